@@ -284,6 +284,166 @@ MXFP4_MOE_API int mxfp4_moe_grad_chain(int32_t T, int32_t H, int32_t E, const ui
                                        const uint16_t* dx, const float* d_logits,
                                        const uint16_t* w_r, uint16_t* g_out, void* stream);
 
+/* ---- expert routing beside the block's own ------------------------------------------------
+ * Routing with the scores, groups and balance bias of MoE models whose router is not a softmax
+ * over the k selected logits (no counterpart in the pages; the block's own routing stays
+ * inside mxfp4_moe_forward).  Per token with logits l [E] and an optional bias b [E]:
+ *     masked(e) = l_e (or b_e) is NaN, -inf or the lowest finite fp32 value
+ *     s_e   = softmax over the unmasked logits (SOFTMAX) or sigmoid(l_e) (SIGMOID); a masked
+ *             logit scores 0; +inf counts as the largest finite value
+ *     key_e = s_e + b_e with a bias, else ordered like l_e.  Keys order the experts only: the
+ *             weights come from s.  Order is decided on fp64 keys: fp32 keys are used where
+ *             their error cannot change it, and the row is redone in fp64 where it could.
+ *     groups > 1: experts [g E/groups, (g+1) E/groups) form group g; its score is the sum of
+ *             its group_best largest keys (s_e without a bias; masked experts are left out),
+ *             and only the top_groups best groups stay eligible (ties to the lower group)
+ *     idx   = the k largest keys among the eligible experts, largest first, ties to the lower
+ *             index.  Masked experts of the kept groups fill up in index order when fewer
+ *             than k are unmasked.
+ *     w_j   = scale * s_j / sum_i s_i (renormalize) or scale * s_j; exactly 0 for a masked
+ *             expert, so a token whose every expert is masked gets k zero weights.
+ * T >= 0, 1 <= k <= E <= 256, 1 <= groups <= 32 dividing E, 1 <= top_groups <= groups with
+ * top_groups * E / groups >= k, group_best 1 or 2 (2 only with E / groups >= 2; ignored with
+ * groups == 1), scale finite and not 0. */
+#define MXFP4_MOE_SCORES_SOFTMAX 0
+#define MXFP4_MOE_SCORES_SIGMOID 1
+typedef struct {
+  int32_t T, E, k;
+  int32_t scores;
+  int32_t groups, top_groups, group_best;
+  int32_t renormalize;
+  float scale;
+} mxfp4_moe_routing;
+
+/*   logits   fp32 [T][E]
+ *   bias     fp32 [E] or NULL: the balance bias
+ *   topk_idx int32 [T][k], topk_w fp32 [T][k]  outputs
+ *   counts   int32 [E] output or NULL: how many of the T*k slots each expert received (what a
+ *            balance-bias update needs); overwritten, not accumulated
+ * Pointers 4-byte aligned.  Errors: INVALID_ARG, UNSUPPORTED_DEVICE, CUDA. */
+MXFP4_MOE_API int mxfp4_moe_route(const mxfp4_moe_routing* r, const float* logits,
+                                  const float* bias, int32_t* topk_idx, float* topk_w,
+                                  int32_t* counts, void* stream);
+
+/* Gradient of the weights with respect to the logits (the selection and the bias carry none).
+ * With p_j = w_j / scale and dw = dL/dw:
+ *     renormalize:  q_j = w_j (dw_j - sum_i p_i dw_i);  otherwise  q_j = w_j dw_j
+ *     SIGMOID:                 d_l = q_j (1 - sigmoid(l)) at the selected experts, else 0
+ *     SOFTMAX, renormalize:    d_l = q_j at the selected experts, else 0
+ *     SOFTMAX:                 d_l[e] = (q_j if selected) - s_e sum_j q_j for every expert
+ * An expert given twice in a row of topk_idx receives the sum of its slots.  An index outside
+ * [0, E) receives nothing and writes nothing.
+ *   logits, topk_idx, topk_w  as in the forward;  d_topk_w fp32 [T][k];  d_logits fp32 [T][E]
+ *   output (every element written)
+ * Pointers 4-byte aligned.  Errors: INVALID_ARG, UNSUPPORTED_DEVICE, CUDA. */
+MXFP4_MOE_API int mxfp4_moe_route_backward(const mxfp4_moe_routing* r, const float* logits,
+                                           const int32_t* topk_idx, const float* topk_w,
+                                           const float* d_topk_w, float* d_logits, void* stream);
+
+/* mxfp4_moe_forward on a routing that the caller holds (mxfp4_moe_route's, or its own) in place
+ * of the logits: out_t = sum_j topk_w[t][j] y_{t,j} for the experts topk_idx[t][j].
+ *   topk_idx int32 [T][k], topk_w fp32 [T][k]  inputs.  The same expert may stand twice in a
+ *            row.  An index outside [0, E) is recorded in the workspace's error word
+ *            (DEVICE_BOUNDS, tag 0x120) and counts as expert 0 with weight 0.
+ * Everything else as in mxfp4_moe_forward; mxfp4_moe_backward_input follows with d_logits NULL,
+ * and mxfp4_moe_route_backward takes its d_topk_w to the logits.
+ * Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, UNSUPPORTED_DEVICE, CUDA. */
+MXFP4_MOE_API int mxfp4_moe_forward_routed(const mxfp4_moe_dims* d, const mxfp4_moe_weights* w,
+                                           const uint16_t* x, const int32_t* topk_idx,
+                                           const float* topk_w, uint16_t* y, void* ws,
+                                           size_t ws_bytes, void* stream);
+
+/* ---- 8-bit activation checkpoints -----------------------------------------------------------
+ * Rows kept between the forward and the backward at 8.25 bits per feature (no counterpart in
+ * the pages; OCP Microscaling Formats (MX) v1.0 for the encodings).  Blocks of 32 features
+ * share a UE8M0 scale byte; element values:
+ *   E4M3 (MXFP8): e4m3(code) * 2^(byte - 127); the block's scale 2^S is the smallest power of
+ *         two with max|x| <= 448 * 2^S, S in [-126, 120]
+ *   INT8 (MXINT8): code / 64 * 2^(byte - 127), codes in [-127, 127] in two's complement; the
+ *         smallest 2^S with max|x| <= 127 * 2^S, byte = S + 133, S in [-126, 121]
+ * x / 2^S is exact and is rounded once, to nearest even.  A block holding an infinity or NaN
+ * gets scale byte 255 and reads back as NaN; rows within a factor 2 of the largest finite value
+ * saturate at 240 * 2^120 (E4M3) and 127 * 2^121 (INT8), so that finite rows read back finite.
+ *   codes uint8 [T][H], scales uint8 [T][H/32]; codes 16-byte aligned; H a multiple of 32. */
+#define MXFP4_MOE_CHECKPOINT_E4M3 0
+#define MXFP4_MOE_CHECKPOINT_INT8 1
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int32_t format;
+} mxfp4_moe_checkpoint;
+
+/* Element type of activation rows and of norm parameters. */
+#define MXFP4_MOE_ROWS_BF16 0
+#define MXFP4_MOE_ROWS_FP32 1
+
+/* Rows to a checkpoint, and back.  T >= 0, 32 <= H <= 16384, a multiple of 32; rows of
+ * rows_format, 16-byte aligned.  Errors: INVALID_ARG, UNSUPPORTED_DEVICE, CUDA. */
+MXFP4_MOE_API int mxfp4_moe_checkpoint_pack(int32_t T, int32_t H, int32_t rows_format,
+                                            const void* x, const mxfp4_moe_checkpoint* to,
+                                            void* stream);
+MXFP4_MOE_API int mxfp4_moe_checkpoint_unpack(int32_t T, int32_t H, int32_t rows_format,
+                                              const mxfp4_moe_checkpoint* from, void* x,
+                                              void* stream);
+
+/* ---- the norm in front of the block ---------------------------------------------------------
+ * Layer norm or rms norm of each row, with the residual add before it and the 8-bit checkpoint
+ * beside it from one read of the rows (no counterpart in the pages; the pre-norm of the decoder
+ * layers around the MoE block).  Statistics and sums in fp32.
+ *   LAYER: mean = sum x / H, rstd = 1/sqrt(sum (x - mean)^2 / H + eps)
+ *   RMS:   mean = 0,         rstd = 1/sqrt(sum x^2 / H + eps)
+ *   out = (x - mean) rstd weight + bias
+ * T >= 0, 1 <= H <= 16384, eps finite and >= 0.  Rows (x, y, x_out, out, d_out, g, dx) have
+ * type rows_format and are dense; weight and bias [H] have type param_format.  Pointers are
+ * aligned to their element type at least; 16-byte aligned pointers with H a multiple of 8 take
+ * the vector path. */
+#define MXFP4_MOE_NORM_LAYER 0
+#define MXFP4_MOE_NORM_RMS 1
+typedef struct {
+  int32_t T, H;
+  int32_t kind;
+  float eps;
+  int32_t rows_format;
+  int32_t param_format;
+} mxfp4_moe_norm;
+
+/* Forward.  The rows come from x or from a checkpoint (`from`), exactly one of the two.
+ *   y       rows or NULL: a residual; x_out = x + y in fp32, rounded once to rows_format, is
+ *           written and is what the norm and the checkpoint take.  x_out NULL exactly when y is.
+ *   to      NULL, or where the rows (x_out, or x) go as a checkpoint (only with x)
+ *   weight, bias  NULL: 1 and 0
+ *   out     output rows;  mean, rstd  fp32 [T] outputs, may be NULL (the backward needs rstd,
+ *           and for LAYER the mean)
+ * Outputs must not overlap inputs or one another.
+ * Errors: INVALID_ARG, UNSUPPORTED_DEVICE, CUDA. */
+MXFP4_MOE_API int mxfp4_moe_norm_forward(const mxfp4_moe_norm* d, const void* x,
+                                         const mxfp4_moe_checkpoint* from, const void* y,
+                                         const void* weight, const void* bias, void* x_out,
+                                         const mxfp4_moe_checkpoint* to, void* out, float* mean,
+                                         float* rstd, void* stream);
+
+/* Bytes of device scratch of mxfp4_moe_norm_backward with d_weight or d_bias. */
+MXFP4_MOE_API int mxfp4_moe_norm_workspace_size(const mxfp4_moe_norm* d, size_t* bytes);
+
+/* Backward.  With xh = (x - mean) rstd and v = d_out weight:
+ *     dx       = rstd (v - xh mean_H(v xh) [- mean_H(v) for LAYER]) [+ g]   rounded once
+ *     d_weight = sum_t d_out xh,  d_bias = sum_t d_out      fp32 [H], order of the sum fixed
+ *   x or from   the rows the forward normalised (x_out where it added a residual), or their
+ *               checkpoint; mean, rstd the statistics of those rows (of a checkpoint: of the
+ *               forward on the checkpoint).  mean may be NULL for RMS.
+ *   g           rows or NULL: the gradient that reaches the rows past the norm; dx may be g
+ *   dx          output rows;  d_weight, d_bias  outputs or NULL
+ *   ws          scratch of mxfp4_moe_norm_workspace_size bytes, 16-byte aligned; may be NULL
+ *               when d_weight and d_bias are
+ * Other overlaps of outputs with inputs or one another are refused.
+ * Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, UNSUPPORTED_DEVICE, CUDA. */
+MXFP4_MOE_API int mxfp4_moe_norm_backward(const mxfp4_moe_norm* d, const void* d_out,
+                                          const void* x, const mxfp4_moe_checkpoint* from,
+                                          const float* mean, const float* rstd,
+                                          const void* weight, const void* g, void* dx,
+                                          float* d_weight, float* d_bias, void* ws,
+                                          size_t ws_bytes, void* stream);
+
 /* Standalone dequantization (diagnostics and tests): rows of packed MXFP4 -> bf16.
  * Source: "Add MXFP4 training support via a dequantize-on-the-fly fallback", section "What this does" (`_dequantize_weights`); OCP MX v1.0.
  *   blocks uint8 [rows][K/2], scales uint8 [rows][K/32], out bf16 [rows][K]; K multiple of 32.

@@ -45,6 +45,30 @@ class Weights(ctypes.Structure):
                 ("dn_blocks", _vp), ("dn_scales", _vp), ("dn_bias", _vp)]
 
 
+SCORES = {"softmax": 0, "sigmoid": 1}
+CHECKPOINTS = {"e4m3": 0, "int8": 1}
+NORMS = {"layer": 0, "rms": 1}
+ROWS_BF16 = 0
+ROWS_FP32 = 1
+
+
+class Routing(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("scores", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Checkpoint(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("format", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("rows_format", ctypes.c_int32),
+                ("param_format", ctypes.c_int32)]
+
+
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int32),
                 ("total_ms", ctypes.c_double)]
@@ -70,6 +94,22 @@ SIGNATURES = {
                                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mxfp4_moe_grad_chain": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                             _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mxfp4_moe_forward_routed": (ctypes.c_int, [ctypes.POINTER(Dims), ctypes.POINTER(Weights), _vp,
+                                                _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mxfp4_moe_route": (ctypes.c_int, [ctypes.POINTER(Routing), _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mxfp4_moe_route_backward": (ctypes.c_int, [ctypes.POINTER(Routing), _vp, _vp, _vp, _vp, _vp,
+                                                _vp]),
+    "mxfp4_moe_checkpoint_pack": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                 _vp, ctypes.POINTER(Checkpoint), _vp]),
+    "mxfp4_moe_checkpoint_unpack": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                   ctypes.POINTER(Checkpoint), _vp, _vp]),
+    "mxfp4_moe_norm_forward": (ctypes.c_int, [ctypes.POINTER(Norm), _vp,
+                                              ctypes.POINTER(Checkpoint), _vp, _vp, _vp, _vp,
+                                              ctypes.POINTER(Checkpoint), _vp, _vp, _vp, _vp]),
+    "mxfp4_moe_norm_workspace_size": (ctypes.c_int, [ctypes.POINTER(Norm), ctypes.POINTER(_sz)]),
+    "mxfp4_moe_norm_backward": (ctypes.c_int, [ctypes.POINTER(Norm), _vp, _vp,
+                                               ctypes.POINTER(Checkpoint), _vp, _vp, _vp, _vp,
+                                               _vp, _vp, _vp, _vp, _sz, _vp]),
     "mxfp4_moe_check": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(ctypes.c_int32)]),
     "mxfp4_moe_selftest_wait_timeout": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp]),
     "mxfp4_moe_interleave_gate_up": (ctypes.c_int, [ctypes.POINTER(Dims), _vp, _vp, _vp, _vp, _vp,

@@ -23,8 +23,9 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmxfp4_moe.so")
 LIB_DEBUG = os.path.join(HERE, "libmxfp4_moe_debug.so")
 SOURCES = ["csrc/api.cu", "csrc/grouped_gemm.cu", "csrc/kernels_small.cu",
-           "csrc/forward_static.cu", "csrc/selftest.cu", "csrc/residual_router.cu"]
-DEPS = SOURCES + ["csrc/common.cuh", "csrc/kernels.h", "csrc/aux_kernels.h"]
+           "csrc/forward_static.cu", "csrc/selftest.cu", "csrc/residual_router.cu",
+           "csrc/routing.cu", "csrc/norm.cu"]
+DEPS = SOURCES + ["csrc/common.cuh", "csrc/kernels.h", "csrc/aux_kernels.h", "csrc/block_edge.h"]
 
 
 def nvcc() -> str:

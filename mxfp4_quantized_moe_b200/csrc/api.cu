@@ -10,6 +10,7 @@
 #include "../../include/mxfp4_moe.h"
 #include "kernels.h"
 #include "aux_kernels.h"
+#include "block_edge.h"
 
 namespace {
 
@@ -67,6 +68,8 @@ WtLayout wt_layout(const mxfp4_moe_dims& d) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
 int check_dims(const mxfp4_moe_dims* d) {
   if (!d) return MXFP4_MOE_ERR_INVALID_ARG;
@@ -192,6 +195,118 @@ struct Timed {
     MOE_TRY(expr);               \
   } while (0)
 
+// The forward behind the routing: idx, w and the segments' histograms are in the workspace.
+int forward_experts(const mxfp4_moe_dims& dims, const mxfp4_moe_weights& weights,
+                    const uint16_t* x, uint16_t* y, void* ws, const WsLayout& L, int sms,
+                    cudaStream_t st) {
+  const mxfp4_moe_dims* d = &dims;
+  const mxfp4_moe_weights* w = &weights;
+  const int T = d->T, H = d->H, I = d->I, E = d->E, k = d->k, A = T * k;
+  int* err = at<int>(ws, L.err);
+  int32_t* off = at<int32_t>(ws, L.off);
+  int32_t* idx = at<int32_t>(ws, L.idx);
+  float* wr = at<float>(ws, L.w);
+  int32_t* perm = at<int32_t>(ws, L.perm);
+  int32_t* inv = at<int32_t>(ws, L.inv);
+  float* w_row = at<float>(ws, L.w_row);
+  int32_t* blk_hist = at<int32_t>(ws, L.blk_hist);
+  uint16_t* dgu = at<uint16_t>(ws, L.dgu);
+  uint16_t* act = at<uint16_t>(ws, L.act);
+  uint16_t* rows = at<uint16_t>(ws, L.rows);
+
+  MOE_LAUNCH("seg_scan", moe::launch_seg_scan(T, E, blk_hist, st));
+  MOE_LAUNCH("build_perm", moe::launch_build_perm(idx, wr, T, E, k, blk_hist, off, perm, inv, w_row, err, st));
+  const bool bs = d->gate_up_format == MXFP4_MOE_GATE_UP_BLOCK_SCALED;
+  // Xp in expert-sorted order: bf16 rows (in `rows`, which the down GEMM overwrites with y), or
+  // as two E4M3 parts (hi | lo in the dH region, free until the backward) with UE8M0 scales
+  uint8_t* xhi = at<uint8_t>(ws, L.dh);
+  uint8_t* xlo = xhi + (size_t)A * H;
+  uint8_t* sfb = at<uint8_t>(ws, L.sfb);
+  if (bs)
+    MOE_LAUNCH("gather_x_mx", moe::launch_gather_quant(x, H, k, perm, A, xhi, xlo, sfb, sfb_stride(H), err, st));
+  else
+    MOE_LAUNCH("gather_x", moe::launch_gather_rows(x, H, k, perm, A, rows, nullptr, err, st));
+
+  moe::GemmArgs g{};
+  g.off = off; g.E = E; g.A = A; g.err = err;
+  g.alpha = d->glu_alpha; g.limit = d->glu_limit; g.mask_limit = bf16_mask_limit(d->glu_limit);
+  // gate_up: h = Xp W_gu^T + b_gu; act = GLU(h) and the GLU derivative factors are saved
+  // (block-scaled: E2M1 weights against the E4M3 parts; both forms accumulate in fp32)
+  g.scales = w->gu_scales; g.K = H; g.N = 2 * I; g.bias = w->gu_bias; g.out0 = dgu; g.out1 = act;
+  if (bs) {
+    g.tok_lo = xlo; g.sfb = sfb; g.sfb_stride = sfb_stride(H);
+    MOE_LAUNCH("gemm_gate_up_glu", moe::launch_grouped_gemm(moe::kEpiGateUp, false, xhi, w->gu_blocks, g, sms, st));
+    g.tok_lo = nullptr; g.sfb = nullptr; g.sfb_stride = 0;
+  } else {
+    MOE_LAUNCH("gemm_gate_up_glu", moe::launch_grouped_gemm(moe::kEpiGateUp, false, rows, w->gu_blocks, g, sms, st));
+  }
+  // down: y = act W_d^T + b_d per sorted row (kept for the backward's routing-weight gradient)
+  g.scales = w->dn_scales; g.K = I; g.N = H; g.bias = w->dn_bias; g.out0 = rows; g.out1 = nullptr;
+  MOE_LAUNCH("gemm_down", moe::launch_grouped_gemm(moe::kEpiDown, false, act, w->dn_blocks, g, sms, st));
+  // out_t = sum_j w_{t,j} y_{t,j}
+  MOE_LAUNCH("combine_y", moe::launch_combine(rows, inv, wr, T, k, H, y, err, st));
+  return MXFP4_MOE_OK;
+}
+
+// ---- checks of the operators at the block's edge --------------------------------------
+int check_routing(const mxfp4_moe_routing* r) {
+  if (!r || r->T < 0 || r->E < 1 || r->E > 256 || r->k < 1 || r->k > r->E)
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  if (r->scores != MXFP4_MOE_SCORES_SOFTMAX && r->scores != MXFP4_MOE_SCORES_SIGMOID)
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  if (r->groups < 1 || r->groups > 32 || r->E % r->groups || r->top_groups < 1 ||
+      r->top_groups > r->groups || r->top_groups * (r->E / r->groups) < r->k)
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  if (r->group_best != 1 && r->group_best != 2) return MXFP4_MOE_ERR_INVALID_ARG;
+  if (r->groups > 1 && r->group_best > r->E / r->groups) return MXFP4_MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(r->scale) || r->scale == 0.f) return MXFP4_MOE_ERR_INVALID_ARG;
+  return MXFP4_MOE_OK;
+}
+
+constexpr int kMaxRow = 16384;  // features of a row that one block holds in registers
+
+bool valid_rows(int32_t f) { return f == MXFP4_MOE_ROWS_BF16 || f == MXFP4_MOE_ROWS_FP32; }
+
+bool valid_checkpoint(const mxfp4_moe_checkpoint* c, int H) {
+  return c && c->codes && c->scales && aligned16(c->codes) && H >= 32 && H % 32 == 0 &&
+         H <= kMaxRow &&
+         (c->format == MXFP4_MOE_CHECKPOINT_E4M3 || c->format == MXFP4_MOE_CHECKPOINT_INT8);
+}
+
+int check_norm(const mxfp4_moe_norm* d) {
+  if (!d || d->T < 0 || d->H < 1 || d->H > kMaxRow || !valid_rows(d->rows_format) ||
+      !valid_rows(d->param_format))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  if (d->kind != MXFP4_MOE_NORM_LAYER && d->kind != MXFP4_MOE_NORM_RMS)
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  return std::isfinite(d->eps) && d->eps >= 0.f ? MXFP4_MOE_OK : MXFP4_MOE_ERR_INVALID_ARG;
+}
+
+size_t row_bytes(int T, int H, int32_t format) {
+  return (size_t)T * H * (format == MXFP4_MOE_ROWS_FP32 ? 4 : 2);
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && pa < pb + nb && pb < pa + na;
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+// An output over an input, or over another output.
+template <size_t NI, size_t NO>
+bool any_overlap(const Span (&in)[NI], const Span (&out)[NO]) {
+  for (size_t o = 0; o < NO; ++o) {
+    for (const Span& i : in)
+      if (overlap(out[o].p, out[o].n, i.p, i.n)) return true;
+    for (size_t q = o + 1; q < NO; ++q)
+      if (overlap(out[o].p, out[o].n, out[q].p, out[q].n)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -245,52 +360,27 @@ int mxfp4_moe_forward(const mxfp4_moe_dims* d, const mxfp4_moe_weights* w, const
   rc = check_device(&sms);
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int T = d->T, H = d->H, I = d->I, E = d->E, k = d->k, A = T * k;
-  int* err = at<int>(ws, L.err);
-  int32_t* off = at<int32_t>(ws, L.off);
-  int32_t* idx = at<int32_t>(ws, L.idx);
-  float* wr = at<float>(ws, L.w);
-  int32_t* perm = at<int32_t>(ws, L.perm);
-  int32_t* inv = at<int32_t>(ws, L.inv);
-  float* w_row = at<float>(ws, L.w_row);
-  int32_t* blk_hist = at<int32_t>(ws, L.blk_hist);
-  uint16_t* dgu = at<uint16_t>(ws, L.dgu);
-  uint16_t* act = at<uint16_t>(ws, L.act);
-  uint16_t* rows = at<uint16_t>(ws, L.rows);
+  MOE_LAUNCH("router_topk", moe::launch_router_topk(logits, d->T, d->E, d->k, at<int32_t>(ws, L.idx), at<float>(ws, L.w), at<int32_t>(ws, L.blk_hist), topk_idx, topk_w, st));
+  return forward_experts(*d, *w, x, y, ws, L, sms, st);
+}
 
-  MOE_LAUNCH("router_topk", moe::launch_router_topk(logits, T, E, k, idx, wr, blk_hist, topk_idx, topk_w, st));
-  MOE_LAUNCH("seg_scan", moe::launch_seg_scan(T, E, blk_hist, st));
-  MOE_LAUNCH("build_perm", moe::launch_build_perm(idx, wr, T, E, k, blk_hist, off, perm, inv, w_row, err, st));
-  const bool bs = d->gate_up_format == MXFP4_MOE_GATE_UP_BLOCK_SCALED;
-  // Xp in expert-sorted order: bf16 rows (in `rows`, which the down GEMM overwrites with y), or
-  // as two E4M3 parts (hi | lo in the dH region, free until the backward) with UE8M0 scales
-  uint8_t* xhi = at<uint8_t>(ws, L.dh);
-  uint8_t* xlo = xhi + (size_t)A * H;
-  uint8_t* sfb = at<uint8_t>(ws, L.sfb);
-  if (bs)
-    MOE_LAUNCH("gather_x_mx", moe::launch_gather_quant(x, H, k, perm, A, xhi, xlo, sfb, sfb_stride(H), err, st));
-  else
-    MOE_LAUNCH("gather_x", moe::launch_gather_rows(x, H, k, perm, A, rows, nullptr, err, st));
-
-  moe::GemmArgs g{};
-  g.off = off; g.E = E; g.A = A; g.err = err;
-  g.alpha = d->glu_alpha; g.limit = d->glu_limit; g.mask_limit = bf16_mask_limit(d->glu_limit);
-  // gate_up: h = Xp W_gu^T + b_gu; act = GLU(h) and the GLU derivative factors are saved
-  // (block-scaled: E2M1 weights against the E4M3 parts; both forms accumulate in fp32)
-  g.scales = w->gu_scales; g.K = H; g.N = 2 * I; g.bias = w->gu_bias; g.out0 = dgu; g.out1 = act;
-  if (bs) {
-    g.tok_lo = xlo; g.sfb = sfb; g.sfb_stride = sfb_stride(H);
-    MOE_LAUNCH("gemm_gate_up_glu", moe::launch_grouped_gemm(moe::kEpiGateUp, false, xhi, w->gu_blocks, g, sms, st));
-    g.tok_lo = nullptr; g.sfb = nullptr; g.sfb_stride = 0;
-  } else {
-    MOE_LAUNCH("gemm_gate_up_glu", moe::launch_grouped_gemm(moe::kEpiGateUp, false, rows, w->gu_blocks, g, sms, st));
-  }
-  // down: y = act W_d^T + b_d per sorted row (kept for the backward's routing-weight gradient)
-  g.scales = w->dn_scales; g.K = I; g.N = H; g.bias = w->dn_bias; g.out0 = rows; g.out1 = nullptr;
-  MOE_LAUNCH("gemm_down", moe::launch_grouped_gemm(moe::kEpiDown, false, act, w->dn_blocks, g, sms, st));
-  // out_t = sum_j w_{t,j} y_{t,j}
-  MOE_LAUNCH("combine_y", moe::launch_combine(rows, inv, wr, T, k, H, y, err, st));
-  return MXFP4_MOE_OK;
+int mxfp4_moe_forward_routed(const mxfp4_moe_dims* d, const mxfp4_moe_weights* w,
+                             const uint16_t* x, const int32_t* topk_idx, const float* topk_w,
+                             uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_dims(d);
+  if (!rc) rc = check_weights(w);
+  if (rc) return rc;
+  if (!x || !topk_idx || !topk_w || !y || !ws || !aligned16(x) || !aligned16(y) ||
+      !aligned16(ws) || !aligned4(topk_idx) || !aligned4(topk_w))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const WsLayout L = ws_layout(*d);
+  if (ws_bytes < L.total) return MXFP4_MOE_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  rc = check_device(&sms);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_LAUNCH("import_routing", moe::launch_import_routing(topk_idx, topk_w, d->T, d->E, d->k, at<int32_t>(ws, L.idx), at<float>(ws, L.w), at<int32_t>(ws, L.blk_hist), at<int>(ws, L.err), st));
+  return forward_experts(*d, *w, x, y, ws, L, sms, st);
 }
 
 int mxfp4_moe_backward_input(const mxfp4_moe_dims* d, const mxfp4_moe_weights* w,
@@ -424,6 +514,172 @@ int mxfp4_moe_grad_chain(int32_t T, int32_t H, int32_t E, const uint16_t* g, con
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   MOE_LAUNCH("grad_chain", moe::launch_grad_chain(T, H, E, g, dx, d_logits, w_r, g_out, st));
+  return MXFP4_MOE_OK;
+}
+
+int mxfp4_moe_route(const mxfp4_moe_routing* r, const float* logits, const float* bias,
+                    int32_t* topk_idx, float* topk_w, int32_t* counts, void* stream) {
+  int rc = check_routing(r);
+  if (rc) return rc;
+  if (!logits || !topk_idx || !topk_w || !aligned4(logits) || !aligned4(bias) ||
+      !aligned4(topk_idx) || !aligned4(topk_w) || !aligned4(counts))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const size_t E4 = 4 * (size_t)r->E, m = 4 * (size_t)r->T * r->k;
+  const Span in[] = {{logits, r->T * E4}, {bias, E4}};
+  const Span outs[] = {{topk_idx, m}, {topk_w, m}, {counts, E4}};
+  if (any_overlap(in, outs)) return MXFP4_MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = check_device(&sms);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_LAUNCH("route", moe::launch_route(*r, logits, bias, topk_idx, topk_w, counts, sms, st));
+  return MXFP4_MOE_OK;
+}
+
+int mxfp4_moe_route_backward(const mxfp4_moe_routing* r, const float* logits,
+                             const int32_t* topk_idx, const float* topk_w,
+                             const float* d_topk_w, float* d_logits, void* stream) {
+  int rc = check_routing(r);
+  if (rc) return rc;
+  if (!logits || !topk_idx || !topk_w || !d_topk_w || !d_logits || !aligned4(logits) ||
+      !aligned4(topk_idx) || !aligned4(topk_w) || !aligned4(d_topk_w) || !aligned4(d_logits))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const size_t n = 4 * (size_t)r->T * r->E, m = 4 * (size_t)r->T * r->k;
+  const Span in[] = {{logits, n}, {topk_idx, m}, {topk_w, m}, {d_topk_w, m}};
+  const Span outs[] = {{d_logits, n}};
+  if (any_overlap(in, outs)) return MXFP4_MOE_ERR_INVALID_ARG;
+  rc = check_device(nullptr);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_LAUNCH("route_backward",
+             moe::launch_route_backward(*r, logits, topk_idx, topk_w, d_topk_w, d_logits, st));
+  return MXFP4_MOE_OK;
+}
+
+int mxfp4_moe_checkpoint_pack(int32_t T, int32_t H, int32_t rows_format, const void* x,
+                              const mxfp4_moe_checkpoint* to, void* stream) {
+  if (T < 0 || !valid_rows(rows_format) || !x || !aligned16(x) || !valid_checkpoint(to, H))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const size_t n = row_bytes(T, H, rows_format), c = (size_t)T * H;
+  const Span in[] = {{x, n}};
+  const Span outs[] = {{to->codes, c}, {to->scales, c / 32}};
+  if (any_overlap(in, outs)) return MXFP4_MOE_ERR_INVALID_ARG;
+  const int rc = check_device(nullptr);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_LAUNCH("checkpoint_pack",
+             moe::launch_checkpoint_pack(T, H, rows_format == MXFP4_MOE_ROWS_FP32, x, *to, st));
+  return MXFP4_MOE_OK;
+}
+
+int mxfp4_moe_checkpoint_unpack(int32_t T, int32_t H, int32_t rows_format,
+                                const mxfp4_moe_checkpoint* from, void* x, void* stream) {
+  if (T < 0 || !valid_rows(rows_format) || !x || !aligned16(x) || !valid_checkpoint(from, H))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const size_t n = row_bytes(T, H, rows_format), c = (size_t)T * H;
+  const Span in[] = {{from->codes, c}, {from->scales, c / 32}};
+  const Span outs[] = {{x, n}};
+  if (any_overlap(in, outs)) return MXFP4_MOE_ERR_INVALID_ARG;
+  const int rc = check_device(nullptr);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_LAUNCH("checkpoint_unpack",
+             moe::launch_checkpoint_unpack(T, H, rows_format == MXFP4_MOE_ROWS_FP32, *from, x, st));
+  return MXFP4_MOE_OK;
+}
+
+int mxfp4_moe_norm_forward(const mxfp4_moe_norm* d, const void* x,
+                           const mxfp4_moe_checkpoint* from, const void* y, const void* weight,
+                           const void* bias, void* x_out, const mxfp4_moe_checkpoint* to,
+                           void* out, float* mean, float* rstd, void* stream) {
+  int rc = check_norm(d);
+  if (rc) return rc;
+  if ((x == nullptr) == (from == nullptr) || (y == nullptr) != (x_out == nullptr) || !out)
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  if (from && (y || to)) return MXFP4_MOE_ERR_INVALID_ARG;
+  if ((from && !valid_checkpoint(from, d->H)) || (to && !valid_checkpoint(to, d->H)))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const bool f32 = d->rows_format == MXFP4_MOE_ROWS_FP32;
+  const bool p32 = d->param_format == MXFP4_MOE_ROWS_FP32;
+  auto elem = [](const void* p, bool wide) { return wide ? aligned4(p) : aligned2(p); };
+  if (!elem(x, f32) || !elem(y, f32) || !elem(x_out, f32) || !elem(out, f32) ||
+      !elem(weight, p32) || !elem(bias, p32) || !aligned4(mean) || !aligned4(rstd))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  if ((from || to) && !(aligned16(x) && aligned16(y) && aligned16(x_out) && aligned16(out) &&
+                        aligned16(weight) && aligned16(bias)))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const size_t n = row_bytes(d->T, d->H, d->rows_format), c = (size_t)d->T * d->H;
+  const size_t pb = row_bytes(1, d->H, d->param_format), s = 4 * (size_t)d->T;
+  const Span in[] = {{x, n}, {y, n}, {weight, pb}, {bias, pb},
+                     {from ? from->codes : nullptr, c}, {from ? from->scales : nullptr, c / 32}};
+  const Span outs[] = {{x_out, n}, {out, n}, {mean, s}, {rstd, s},
+                       {to ? to->codes : nullptr, c}, {to ? to->scales : nullptr, c / 32}};
+  if (any_overlap(in, outs)) return MXFP4_MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = check_device(&sms);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  moe::NormArgs a{};
+  a.T = d->T; a.H = d->H; a.rms = d->kind == MXFP4_MOE_NORM_RMS; a.rows_f32 = f32;
+  a.param_f32 = p32; a.eps = d->eps;
+  a.x = x; a.y = y; a.weight = weight; a.bias = bias; a.x_out = x_out; a.out = out;
+  a.mean = mean; a.rstd = rstd;
+  if (from) a.from = *from;
+  if (to) a.to = *to;
+  MOE_LAUNCH("norm_forward", moe::launch_norm_forward(a, sms, st));
+  return MXFP4_MOE_OK;
+}
+
+int mxfp4_moe_norm_workspace_size(const mxfp4_moe_norm* d, size_t* bytes) {
+  const int rc = check_norm(d);
+  if (rc) return rc;
+  if (!bytes) return MXFP4_MOE_ERR_INVALID_ARG;
+  *bytes = moe::norm_scratch_bytes(d->T, d->H);
+  return MXFP4_MOE_OK;
+}
+
+int mxfp4_moe_norm_backward(const mxfp4_moe_norm* d, const void* d_out, const void* x,
+                            const mxfp4_moe_checkpoint* from, const float* mean,
+                            const float* rstd, const void* weight, const void* g, void* dx,
+                            float* d_weight, float* d_bias, void* ws, size_t ws_bytes,
+                            void* stream) {
+  int rc = check_norm(d);
+  if (rc) return rc;
+  if (!d_out || (x == nullptr) == (from == nullptr) || !rstd || !dx ||
+      (d->kind == MXFP4_MOE_NORM_LAYER && !mean) || (from && !valid_checkpoint(from, d->H)))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const bool f32 = d->rows_format == MXFP4_MOE_ROWS_FP32;
+  const bool p32 = d->param_format == MXFP4_MOE_ROWS_FP32;
+  auto elem = [](const void* p, bool wide) { return wide ? aligned4(p) : aligned2(p); };
+  if (!elem(d_out, f32) || !elem(x, f32) || !elem(g, f32) || !elem(dx, f32) ||
+      !elem(weight, p32) || !aligned4(mean) || !aligned4(rstd) || !aligned4(d_weight) ||
+      !aligned4(d_bias) || !aligned16(ws))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  if (from && !(aligned16(d_out) && aligned16(g) && aligned16(dx) && aligned16(weight)))
+    return MXFP4_MOE_ERR_INVALID_ARG;
+  const bool params = d_weight || d_bias;
+  const size_t need = params ? moe::norm_scratch_bytes(d->T, d->H) : 0;
+  if (need && !ws) return MXFP4_MOE_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MXFP4_MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t n = row_bytes(d->T, d->H, d->rows_format), c = (size_t)d->T * d->H;
+  const size_t pb = row_bytes(1, d->H, d->param_format), s = 4 * (size_t)d->T;
+  const Span in[] = {{d_out, n}, {x, n}, {g == dx ? nullptr : g, n}, {weight, pb}, {mean, s},
+                     {rstd, s}, {from ? from->codes : nullptr, c},
+                     {from ? from->scales : nullptr, c / 32}};
+  const Span outs[] = {{dx, n}, {d_weight, 4 * (size_t)d->H}, {d_bias, 4 * (size_t)d->H},
+                       {need ? ws : nullptr, need}};
+  if (any_overlap(in, outs)) return MXFP4_MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = check_device(&sms);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  moe::NormGradArgs a{};
+  a.T = d->T; a.H = d->H; a.rms = d->kind == MXFP4_MOE_NORM_RMS; a.rows_f32 = f32;
+  a.param_f32 = p32;
+  a.d_out = d_out; a.x = x; a.mean = mean; a.rstd = rstd; a.weight = weight; a.g = g; a.dx = dx;
+  a.d_weight = d_weight; a.d_bias = d_bias; a.partial = static_cast<float*>(ws);
+  if (from) a.from = *from;
+  MOE_LAUNCH("norm_backward", moe::launch_norm_backward(a, sms, st));
   return MXFP4_MOE_OK;
 }
 

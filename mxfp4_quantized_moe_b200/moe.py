@@ -7,8 +7,10 @@ library's kernels.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -216,6 +218,318 @@ def grad_chain(g: torch.Tensor, dx: torch.Tensor, d_logits: torch.Tensor, w_r: t
     check(lib.mxfp4_moe_grad_chain(T, H, E, _ptr(g), _ptr(dx), _ptr(d_logits), _ptr(w_r),
                                    _ptr(out), _stream(stream)), "mxfp4_moe_grad_chain")
     return out
+
+
+# ---- the operators at the block's edge: routing, the norm, 8-bit checkpoints ----------------
+# These run on the device of their tensors (all on one), whichever device is current, on that
+# device's current stream or on `stream`; what they allocate belongs to that stream.  Rows and
+# vectors are dense; every output that a caller may pass is also what the call returns.
+_HERE = contextlib.nullcontext()
+_EMPTY = 256  # stands for the null pointer of a tensor without elements; never dereferenced
+
+
+def _at(device: torch.device, stream):
+    """Where a call on `device` allocates and launches."""
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream and tensors are on different devices")
+        return torch.cuda.stream(stream)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _tensor(t: torch.Tensor, name: str, shape, dtypes, device) -> int:
+    """The data pointer of a dense tensor of that shape, type and device."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or _EMPTY
+
+
+def _output(t: torch.Tensor | None, name: str, shape, dtype, device):
+    """The caller's output, checked, or a new one: (tensor, data pointer)."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr() or _EMPTY
+    return t, _tensor(t, name, shape, (dtype,), device)
+
+
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+_ROWS = (torch.bfloat16, torch.float32)
+
+
+@dataclass(frozen=True)
+class Routing:
+    """How tokens choose their experts (mxfp4_moe_routing in include/mxfp4_moe.h)."""
+    k: int
+    scores: str = "softmax"    # or "sigmoid"
+    groups: int = 1            # experts in equal groups, of which the best `top_groups` stay
+    top_groups: int = 1
+    group_best: int = 1        # 1 or 2: the largest keys that sum to a group's score
+    renormalize: bool = True   # weights divided by the selected scores' sum
+    scale: float = 1.0
+
+    def dims(self, T: int, E: int) -> _lib.Routing:
+        if self.scores not in _lib.SCORES:
+            raise ValueError(f"scores must be one of {sorted(_lib.SCORES)}")
+        return _lib.Routing(T, E, self.k, _lib.SCORES[self.scores], self.groups, self.top_groups,
+                            self.group_best, int(self.renormalize), self.scale)
+
+
+def _logits(logits: torch.Tensor):
+    if logits.dim() != 2:
+        raise ValueError("logits must be fp32 [T, E]")
+    return logits.shape, logits.device
+
+
+def route(routing: Routing, logits: torch.Tensor, bias: torch.Tensor | None = None,
+          topk_idx: torch.Tensor | None = None, topk_w: torch.Tensor | None = None,
+          counts: torch.Tensor | None = None, stream=None):
+    """(topk_idx int32 [T, k], topk_w fp32 [T, k]) of fp32 logits [T, E] and, where given, a
+    balance bias fp32 [E] on the selection.  `counts` (int32 [E]) receives the slots of each
+    expert.  Logits or biases of NaN, -inf or the lowest finite value mask an expert: it is
+    selected last, with weight 0."""
+    (T, E), dev = _logits(logits)
+    with _at(dev, stream):
+        lp = _tensor(logits, "logits", (T, E), _F32, dev)
+        bp = None if bias is None else _tensor(bias, "bias", (E,), _F32, dev)
+        topk_idx, ip = _output(topk_idx, "topk_idx", (T, routing.k), torch.int32, dev)
+        topk_w, wp = _output(topk_w, "topk_w", (T, routing.k), torch.float32, dev)
+        cp = None if counts is None else _tensor(counts, "counts", (E,), _I32, dev)
+        dims = routing.dims(T, E)
+        check(lib.mxfp4_moe_route(dims, lp, bp, ip, wp, cp, _stream()), "mxfp4_moe_route")
+    return topk_idx, topk_w
+
+
+def route_backward(routing: Routing, logits: torch.Tensor, topk_idx: torch.Tensor,
+                   topk_w: torch.Tensor, d_topk_w: torch.Tensor,
+                   d_logits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """d_logits fp32 [T, E] from d_topk_w fp32 [T, k], for what `route` returned on `logits`."""
+    (T, E), dev = _logits(logits)
+    slots = (T, routing.k)
+    with _at(dev, stream):
+        lp = _tensor(logits, "logits", (T, E), _F32, dev)
+        ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
+        wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
+        dp = _tensor(d_topk_w, "d_topk_w", slots, _F32, dev)
+        d_logits, op = _output(d_logits, "d_logits", (T, E), torch.float32, dev)
+        dims = routing.dims(T, E)
+        check(lib.mxfp4_moe_route_backward(dims, lp, ip, wp, dp, op, _stream()),
+              "mxfp4_moe_route_backward")
+    return d_logits
+
+
+def forward_routed(shape: MoeShape, w: dict, x: torch.Tensor, topk_idx: torch.Tensor,
+                   topk_w: torch.Tensor, ws: torch.Tensor, y: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The block's forward on a given routing in place of its own (topk_idx int32 and topk_w fp32
+    [T, k]).  `backward_input(..., want_d_logits=False)` follows it; its d_topk_w goes on to
+    `route_backward`."""
+    dev = x.device
+    slots = (shape.T, shape.k)
+    with _at(dev, stream):
+        xp = _tensor(x, "x", (shape.T, shape.H), (torch.bfloat16,), dev)
+        ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
+        wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
+        if ws.device != dev:
+            raise ValueError(f"ws is on {ws.device}, expected {dev}")
+        y, yp = _output(y, "y", (shape.T, shape.H), torch.bfloat16, dev)
+        check(lib.mxfp4_moe_forward_routed(shape.dims(), _weights(w), xp, ip, wp, yp, _ptr(ws),
+                                           ws.numel() * ws.element_size(), _stream()),
+              "mxfp4_moe_forward_routed")
+    return y
+
+
+@dataclass
+class Checkpoint:
+    """Rows in 8 bits: codes uint8 [T, H] and a UE8M0 scale uint8 [T, H/32] per 32 features;
+    format "e4m3" (MXFP8) or "int8" (MXINT8)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    format: str = "e4m3"
+
+    @staticmethod
+    def empty(T: int, H: int, format: str = "e4m3", device="cuda") -> "Checkpoint":
+        if H % 32:
+            raise ValueError("a checkpoint needs H to be a multiple of 32")
+        return Checkpoint(torch.empty(T, H, dtype=torch.uint8, device=device),
+                          torch.empty(T, H // 32, dtype=torch.uint8, device=device), format)
+
+    def _abi(self, T: int, H: int, device) -> _lib.Checkpoint:
+        if self.format not in _lib.CHECKPOINTS:
+            raise ValueError(f"format must be one of {sorted(_lib.CHECKPOINTS)}")
+        return _lib.Checkpoint(_tensor(self.codes, "codes", (T, H), _U8, device),
+                               _tensor(self.scales, "scales", (T, H // 32), _U8, device),
+                               _lib.CHECKPOINTS[self.format])
+
+
+def _rows_shape(x):
+    t = x.codes if isinstance(x, Checkpoint) else x
+    if t.dim() != 2:
+        raise ValueError("rows must be [T, H]")
+    return t.shape[0], t.shape[1], t.device
+
+
+def _format(dtype: torch.dtype) -> int:
+    if dtype not in _ROWS:
+        raise TypeError(f"expected bf16 or fp32, not {dtype}")
+    return _lib.ROWS_FP32 if dtype == torch.float32 else _lib.ROWS_BF16
+
+
+def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | None = None,
+                    stream=None) -> Checkpoint:
+    """Rows [T, H] (bf16 or fp32, H a multiple of 32) stored in 8 bits."""
+    T, H, dev = _rows_shape(x)
+    with _at(dev, stream):
+        xp = _tensor(x, "x", (T, H), _ROWS, dev)
+        if out is None:
+            out = Checkpoint.empty(T, H, format, dev)
+        to = out._abi(T, H, dev)
+        check(lib.mxfp4_moe_checkpoint_pack(T, H, _format(x.dtype), xp, to, _stream()),
+              "mxfp4_moe_checkpoint_pack")
+    return out
+
+
+def checkpoint_unpack(checkpoint: Checkpoint, dtype: torch.dtype = torch.bfloat16,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The rows [T, H] that a checkpoint stands for, as bf16 or fp32."""
+    T, H, dev = _rows_shape(checkpoint)
+    with _at(dev, stream):
+        fmt = _format(dtype)
+        frm = checkpoint._abi(T, H, dev)
+        out, op = _output(out, "out", (T, H), dtype, dev)
+        check(lib.mxfp4_moe_checkpoint_unpack(T, H, fmt, frm, op, _stream()),
+              "mxfp4_moe_checkpoint_unpack")
+    return out
+
+
+class NormOut(NamedTuple):
+    out: torch.Tensor
+    x_out: torch.Tensor | None          # x + y, where y was given
+    mean: torch.Tensor | None           # fp32 [T]; None for "rms"
+    rstd: torch.Tensor                  # fp32 [T]
+    checkpoint: Checkpoint | None       # where one was asked for
+
+
+def _norm_dims(T, H, kind, eps, rows, weight, bias) -> _lib.Norm:
+    if kind not in _lib.NORMS:
+        raise ValueError(f"kind must be one of {sorted(_lib.NORMS)}")
+    p = weight if weight is not None else bias
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same type")
+    return _lib.Norm(T, H, _lib.NORMS[kind], eps, _format(rows),
+                     _lib.ROWS_BF16 if p is None else _format(p.dtype))
+
+
+def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = None,
+                 bias: torch.Tensor | None = None, *, kind: str = "layer", eps: float = 1e-5,
+                 y: torch.Tensor | None = None, checkpoint: str | Checkpoint | None = None,
+                 dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                 x_out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                 rstd: torch.Tensor | None = None, stream=None) -> NormOut:
+    """Layer norm (kind "layer") or rms norm ("rms") of rows [T, H] in one kernel.
+
+    x: bf16 or fp32 rows, or a Checkpoint (normalised as the rows it stands for, into `dtype`,
+    bf16 by default).  y: a residual; x_out = x + y, rounded to the rows' type, is returned and
+    is what is normalised.  checkpoint: a format or a Checkpoint to fill with those rows."""
+    T, H, dev = _rows_shape(x)
+    stored = isinstance(x, Checkpoint)
+    if stored:
+        if y is not None or checkpoint is not None:
+            raise ValueError("a checkpoint as input takes no residual and fills no checkpoint")
+        dtype = torch.bfloat16 if dtype is None else dtype
+    elif dtype is not None and dtype != x.dtype:
+        raise ValueError("dtype is the rows' own type, except for a checkpoint")
+    else:
+        dtype = x.dtype
+    if y is None and x_out is not None:
+        raise ValueError("x_out without a residual")
+    dims = _norm_dims(T, H, kind, eps, dtype, weight, bias)
+    with _at(dev, stream):
+        if stored:
+            xp, frm = None, x._abi(T, H, dev)
+        else:
+            xp, frm = _tensor(x, "x", (T, H), _ROWS, dev), None
+        yp = op = mp = to = None
+        wp = None if weight is None else _tensor(weight, "weight", (H,), _ROWS, dev)
+        bp = None if bias is None else _tensor(bias, "bias", (H,), _ROWS, dev)
+        if y is not None:
+            yp = _tensor(y, "y", (T, H), (dtype,), dev)
+            x_out, op = _output(x_out, "x_out", (T, H), dtype, dev)
+        if checkpoint is not None:
+            if not isinstance(checkpoint, Checkpoint):
+                checkpoint = Checkpoint.empty(T, H, checkpoint, dev)
+            to = checkpoint._abi(T, H, dev)
+        out, np_ = _output(out, "out", (T, H), dtype, dev)
+        if kind == "layer" or mean is not None:
+            mean, mp = _output(mean, "mean", (T,), torch.float32, dev)
+        rstd, rp = _output(rstd, "rstd", (T,), torch.float32, dev)
+        check(lib.mxfp4_moe_norm_forward(dims, xp, frm, yp, wp, bp, op, to, np_, mp, rp,
+                                         _stream()), "mxfp4_moe_norm_forward")
+    return NormOut(out, x_out, mean, rstd, checkpoint)
+
+
+def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch.Tensor | None,
+                  rstd: torch.Tensor, weight: torch.Tensor | None = None, *, kind: str = "layer",
+                  g: torch.Tensor | None = None, params: bool = True,
+                  dx: torch.Tensor | None = None, d_weight: torch.Tensor | None = None,
+                  d_bias: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                  stream=None):
+    """(dx [+ g], d_weight, d_bias) of `norm_forward`; the parameters' gradients are fp32 [H].
+
+    x: the rows that were normalised (x_out where a residual was added), or their checkpoint with
+    the statistics of the forward on it.  g: the residual stream's gradient, added to dx (dx may
+    be g itself).  params=False computes dx alone and returns None for the other two; d_bias is
+    None for "rms" unless a tensor is given.  ws: scratch of norm_workspace_bytes (else
+    allocated); two captured graphs that may run at once need one each."""
+    T, H, dev = _rows_shape(x)
+    dtype = d_out.dtype
+    dims = _norm_dims(T, H, kind, 0.0, dtype, weight, None)
+    with _at(dev, stream):
+        dp = _tensor(d_out, "d_out", (T, H), _ROWS, dev)
+        if isinstance(x, Checkpoint):
+            xp, frm = None, x._abi(T, H, dev)
+        else:
+            xp, frm = _tensor(x, "x", (T, H), (dtype,), dev), None
+        if kind == "layer" and mean is None:
+            raise ValueError("the layer norm's backward needs the mean")
+        mp = None if mean is None else _tensor(mean, "mean", (T,), _F32, dev)
+        rp = _tensor(rstd, "rstd", (T,), _F32, dev)
+        wp = None if weight is None else _tensor(weight, "weight", (H,), _ROWS, dev)
+        gp = None if g is None else _tensor(g, "g", (T, H), (dtype,), dev)
+        dx, op = _output(dx, "dx", (T, H), dtype, dev)
+        dwp = dbp = wsp = None
+        ws_bytes = 0
+        if params:
+            d_weight, dwp = _output(d_weight, "d_weight", (H,), torch.float32, dev)
+            if kind == "layer" or d_bias is not None:
+                d_bias, dbp = _output(d_bias, "d_bias", (H,), torch.float32, dev)
+            if ws is None:
+                n = ctypes.c_size_t()
+                check(lib.mxfp4_moe_norm_workspace_size(dims, n), "mxfp4_moe_norm_workspace_size")
+                ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+            elif ws.device != dev:
+                raise ValueError(f"ws is on {ws.device}, expected {dev}")
+            wsp, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        elif d_weight is not None or d_bias is not None:
+            raise ValueError("params=False with an output for the parameters' gradient")
+        check(lib.mxfp4_moe_norm_backward(dims, dp, xp, frm, mp, rp, wp, gp, op, dwp, dbp, wsp,
+                                          ws_bytes, _stream()), "mxfp4_moe_norm_backward")
+    return dx, d_weight, d_bias
+
+
+def norm_workspace_bytes(T: int, H: int) -> int:
+    """Scratch bytes of norm_backward with the parameters' gradients."""
+    n = ctypes.c_size_t()
+    check(lib.mxfp4_moe_norm_workspace_size(_lib.Norm(T, H, 0, 0.0, 0, 0), n),
+          "mxfp4_moe_norm_workspace_size")
+    return n.value
 
 
 def selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:
