@@ -22,31 +22,66 @@ MOE_DEV float warp_sum(float v) {
   return v;
 }
 
+// Two values rounded to bf16 by one instruction.
+MOE_DEV uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // ---- rows of bf16 or fp32 -----------------------------------------------------------------
-// V consecutive features as floats: V = 8 in 16-byte vectors, V = 1 alone.  Loads are plain
-// (not the read-only path): an output may be the same buffer as the gradient it is added to.
-template <bool F32, int V>
-MOE_DEV void load_rows(const void* base, size_t at, float (&v)[V]) {
-  if constexpr (F32) {
-    const float* p = static_cast<const float*>(base) + at;
-    if constexpr (V == 8) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      v[0] = *p;
-    }
+// V consecutive features of a row as they come from memory: V = 8 in 16-byte vectors, V = 1
+// alone.  A pass first issues every load it needs into such registers and only then computes:
+// loads of a row must not wait for one another's arithmetic or stores.
+template <int SRC, int V> struct Raw;
+template <> struct Raw<kBf16, 8> { uint4 q; };
+template <> struct Raw<kBf16, 1> { uint32_t q; };
+template <> struct Raw<kF32, 8> { float4 a, b; };
+template <> struct Raw<kF32, 1> { float a; };
+template <int SRC> struct Raw<SRC, 8> { uint2 q; uint32_t byte; };  // checkpoints
+
+template <int SRC, int V>
+MOE_DEV void fetch(Raw<SRC, V>& r, const void* base, size_t at) {
+  if constexpr (SRC == kF32 && V == 8) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    r.a = __ldg(p);
+    r.b = __ldg(p + 1);
+  } else if constexpr (SRC == kF32) {
+    r.a = __ldg(static_cast<const float*>(base) + at);
+  } else if constexpr (V == 8) {
+    r.q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
   } else {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    if constexpr (V == 8) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
-      v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
-    } else {
-      v[0] = bf16_to_f(*p);
-    }
+    r.q = __ldg(static_cast<const uint16_t*>(base) + at);
   }
 }
+// The same from a buffer that the kernel also writes (a gradient added in place).
+template <int SRC, int V>
+MOE_DEV void fetch_rw(Raw<SRC, V>& r, const void* base, size_t at) {
+  if constexpr (SRC == kF32 && V == 8) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    r.a = p[0];
+    r.b = p[1];
+  } else if constexpr (SRC == kF32) {
+    r.a = static_cast<const float*>(base)[at];
+  } else if constexpr (V == 8) {
+    r.q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+  } else {
+    r.q = static_cast<const uint16_t*>(base)[at];
+  }
+}
+template <int SRC, int V>
+MOE_DEV void clear(Raw<SRC, V>& r) {
+  if constexpr (SRC == kF32 && V == 8) r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f);
+  else if constexpr (SRC == kF32) r.a = 0.f;
+  else if constexpr (SRC == kBf16 && V == 8) r.q = make_uint4(0u, 0u, 0u, 0u);
+  else if constexpr (SRC == kBf16) r.q = 0u;
+  else {
+    r.q = make_uint2(0u, 0u);
+    r.byte = 127u;
+  }
+}
+template <bool F32, int V> using Row = Raw<F32 ? kF32 : kBf16, V>;
+
 template <bool F32, int V>
 MOE_DEV void store_rows(void* base, size_t at, const float (&v)[V]) {
   if constexpr (F32) {
@@ -60,29 +95,39 @@ MOE_DEV void store_rows(void* base, size_t at, const float (&v)[V]) {
   } else {
     uint16_t* p = static_cast<uint16_t*>(base) + at;
     if constexpr (V == 8)
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     else
       *p = f_to_bf16(v[0]);
   }
 }
 // fp32 values as the row type holds them
 template <bool F32, int V>
-MOE_DEV void round_rows(float (&v)[V]) {
-  if constexpr (!F32) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = bf16_to_f(f_to_bf16(v[i]));
+MOE_DEV void into_raw(const float (&v)[V], Row<F32, V>& r) {
+  if constexpr (F32 && V == 8) {
+    r.a = make_float4(v[0], v[1], v[2], v[3]);
+    r.b = make_float4(v[4], v[5], v[6], v[7]);
+  } else if constexpr (F32) {
+    r.a = v[0];
+  } else if constexpr (V == 8) {
+    r.q = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                     pack_bf16(v[6], v[7]));
+  } else {
+    r.q = f_to_bf16(v[0]);
   }
 }
-template <int V>
-MOE_DEV void load_params(const void* base, bool f32, size_t at, float absent, float (&v)[V]) {
-  if (!base) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = absent;
-  } else if (f32) {
-    load_rows<true, V>(base, at, v);
+template <bool F32, int V>
+MOE_DEV void store_raw(void* base, size_t at, const Row<F32, V>& r) {
+  if constexpr (F32 && V == 8) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    p[0] = r.a;
+    p[1] = r.b;
+  } else if constexpr (F32) {
+    static_cast<float*>(base)[at] = r.a;
+  } else if constexpr (V == 8) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = r.q;
   } else {
-    load_rows<false, V>(base, at, v);
+    static_cast<uint16_t*>(base)[at] = (uint16_t)r.q;
   }
 }
 
@@ -162,183 +207,678 @@ MOE_DEV void decode8(uint2 q, uint32_t byte, float (&v)[8]) {
   }
 }
 
-// Rows of a pass from any source, 8 (or 1) features at a time.
+// Loads of a pass's rows from any source, and their values.
 template <int SRC, int V>
-MOE_DEV void load_source(const void* x, const mxfp4_moe_checkpoint& from, size_t at, float (&v)[V]) {
+MOE_DEV void fetch_source(Raw<SRC, V>& r, const void* x, const mxfp4_moe_checkpoint& from, size_t at) {
   if constexpr (SRC == kBf16 || SRC == kF32) {
-    load_rows<SRC == kF32, V>(x, at, v);
+    fetch<SRC, V>(r, x, at);
   } else {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(from.codes + at));
-    decode8<SRC>(q, __ldg(from.scales + at / 32), v);
+    r.q = __ldg(reinterpret_cast<const uint2*>(from.codes + at));
+    r.byte = __ldg(from.scales + at / 32);
+  }
+}
+template <int SRC, int V>
+MOE_DEV void values(const Raw<SRC, V>& r, float (&v)[V]) {
+  if constexpr (SRC == kF32 && V == 8) {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+  } else if constexpr (SRC == kF32) {
+    v[0] = r.a;
+  } else if constexpr (SRC == kBf16 && V == 8) {
+    v[0] = bf16_lo(r.q.x); v[1] = bf16_hi(r.q.x); v[2] = bf16_lo(r.q.y); v[3] = bf16_hi(r.q.y);
+    v[4] = bf16_lo(r.q.z); v[5] = bf16_hi(r.q.z); v[6] = bf16_lo(r.q.w); v[7] = bf16_hi(r.q.w);
+  } else if constexpr (SRC == kBf16) {
+    v[0] = __uint_as_float(r.q << 16);
+  } else {
+    decode8<SRC>(r.q, r.byte, v);
+  }
+}
+template <int V>
+MOE_DEV void load_params(const void* base, bool f32, size_t at, float absent, float (&v)[V]) {
+  if (!base) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = absent;
+  } else if (f32) {
+    Raw<kF32, V> r;
+    fetch<kF32, V>(r, base, at);
+    values<kF32, V>(r, v);
+  } else {
+    Raw<kBf16, V> r;
+    fetch<kBf16, V>(r, base, at);
+    values<kBf16, V>(r, v);
+  }
+}
+
+// Feature of a thread's chunk c: chunks go round the lanes of the row's W warps.
+template <int V>
+MOE_DEV int feature(int c, int W, int wi, int lane) { return V * ((c * W + wi) * 32 + lane); }
+
+MOE_DEV void group_barrier(int id, int W) {  // the W warps of a row
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * W) : "memory");
+}
+
+// V features as fp32 in registers; pairs for the paired fp32 arithmetic where V = 8.
+template <int V> struct Vals { float v[1]; };
+template <> struct Vals<8> { uint64_t p[4]; };
+
+template <int V>
+MOE_DEV void set(Vals<V>& x, const float (&v)[V]) {
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.p[i] = f2(v[2 * i], v[2 * i + 1]);
+  } else {
+    x.v[0] = v[0];
+  }
+}
+template <int V>
+MOE_DEV void get(const Vals<V>& x, float (&v)[V]) {
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = f2lo(x.p[i]);
+      v[2 * i + 1] = f2hi(x.p[i]);
+    }
+  } else {
+    v[0] = x.v[0];
+  }
+}
+// Sums that keep two partial sums (even and odd features) where V = 8.
+struct Pair {
+  uint64_t p = 0;  // two zeros
+  MOE_DEV float sum() const { return f2lo(p) + f2hi(p); }
+};
+template <int V>
+MOE_DEV void add_sum(Pair& s, const Vals<V>& x) {
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.p = f2add(s.p, x.p[i]);
+  } else {
+    s.p = f2(f2lo(s.p) + x.v[0], 0.f);
+  }
+}
+// x - mean, in place, and the sum of its squares
+template <int V>
+MOE_DEV void center(Pair& s, Vals<V>& x, float mean) {
+  if constexpr (V == 8) {
+    const uint64_t m = f2(-mean, -mean);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x.p[i] = f2add(x.p[i], m);
+      s.p = f2fma(x.p[i], x.p[i], s.p);
+    }
+  } else {
+    x.v[0] -= mean;
+    s.p = f2(fmaf(x.v[0], x.v[0], f2lo(s.p)), 0.f);
+  }
+}
+template <int V>
+MOE_DEV void scale_shift(Vals<V>& x, float rstd, const Vals<V>& g, const Vals<V>& b) {
+  if constexpr (V == 8) {
+    const uint64_t r = f2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.p[i] = f2fma(f2mul(x.p[i], r), g.p[i], b.p[i]);
+  } else {
+    x.v[0] = fmaf(x.v[0] * rstd, g.v[0], b.v[0]);
+  }
+}
+
+// Totals of Q values over the warp: lane l ends with that of value l / (32 / Q).
+template <int Q>
+MOE_DEV float fold(float (&q)[Q]) {
+  const int lane = threadIdx.x & 31;
+  int n = Q;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool upper = lane & o;
+#pragma unroll
+      for (int i = 0; i < Q / 2; ++i)
+        if (i < n) {
+          const float mine = upper ? q[i + n] : q[i], other = upper ? q[i] : q[i + n];
+          q[i] = mine + __shfl_xor_sync(kFull, other, o);
+        }
+    } else {
+      q[0] += __shfl_xor_sync(kFull, q[0], o);
+    }
+  }
+  return q[0];
+}
+
+// Eight features of a lane into the checkpoint; all lanes of the warp take part (H is a multiple
+// of 32, so the four lanes of a block are inside the row together).
+MOE_DEV void store_checkpoint(const mxfp4_moe_checkpoint& to, size_t at, bool in, const Vals<8>& v) {
+  float f[8];
+  get<8>(v, f);
+  uint32_t byte;
+  const uint2 q = to.format == MXFP4_MOE_CHECKPOINT_E4M3 ? encode8<kE4m3>(f, byte)
+                                                         : encode8<kInt8>(f, byte);
+  if (in) {
+    *reinterpret_cast<uint2*>(to.codes + at) = q;
+    if ((threadIdx.x & 3) == 0) to.scales[at / 32] = (uint8_t)byte;
   }
 }
 
 // ---- forward --------------------------------------------------------------------------------
-// A row is held in registers by W warps (V NC features a thread), so it is read once for the
-// mean, the variance about that mean and the output.  W = 1 reduces by shuffles alone; larger
-// rows add one exchange through shared memory per statistic behind a barrier of the row's own
-// warps.  Bound by the rows' bytes.
-struct RowGroup {  // the W warps of a row
-  int W, warp, bar;
-  float* buf;  // [2][32] floats of shared memory
-  MOE_DEV float sum(float v, int slot) const {
+// A row is held as fp32 in registers from its one read to its output: mean, then the variance
+// about that mean, then the output.
+
+template <int I> struct Index { static constexpr int value = I; };
+
+// RB rows per group of W warps, every load of a row in flight at once.  Bound by the rows' bytes
+// when enough warps share an SM: a thread holds few vectors of a row (NC), so that registers
+// leave room for some 30 warps, whose rows cover one another's loads and reductions.
+template <int SRC, bool F32, int V, int NC, int RB>
+__global__ void __launch_bounds__(512) norm_forward_kernel(NormArgs a, int W) {
+  __shared__ __align__(16) float s_buf[2][16][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
+  const long long row = ((long long)blockIdx.x * (blockDim.x / (32 * W)) + group) * RB;
+  if (row >= a.T) return;  // whole groups leave together
+  constexpr bool kRows = SRC == kBf16 || SRC == kF32;
+  const float inv_h = 1.f / (float)a.H;
+  const int h0 = V * (wi * NC * 32 + lane);  // the lane's vectors are 32 V features apart
+  bool in[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) in[c] = h0 + 32 * V * c < a.H;
+  auto group_sum = [&](float v, int slot) {
     v = warp_sum(v);
     if (W == 1) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) buf[32 * slot + warp] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * W) : "memory");
-    return warp_sum(lane < W ? buf[32 * slot + lane] : 0.f);
-  }
-};
-
-constexpr int kNormThreads = 512;  // most threads of a block (16 warps)
-
-template <int SRC, bool F32, int V, int NC>
-__global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(NormArgs a, int W) {
-  __shared__ float s_buf[16][64];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = warp / W, wi = warp % W;
-  const long long row = (long long)blockIdx.x * (blockDim.x / (32 * W)) + group;
-  if (row >= a.T) return;  // whole groups leave together
-  const RowGroup rg{W, wi, 1 + group, s_buf[group]};
-  const size_t r0 = (size_t)row * a.H;
-  float v[NC][V];
-  float part = 0.f;
+    if (lane == 0) s_buf[slot][group][wi] = v;
+    group_barrier(1 + group, W);
+    const float4* b = reinterpret_cast<const float4*>(s_buf[slot][group]);
+    float t = 0.f;
+    for (int i = 0; i < W; i += 4) {
+      const float4 f = b[i / 4];
+      t += f.x;
+      if (i + 1 < W) t += f.y;
+      if (i + 2 < W) t += f.z;
+      if (i + 3 < W) t += f.w;
+    }
+    return t;
+  };
+  Vals<V> v[RB][NC];
+  {
+    Raw<SRC, V> r[RB][NC];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int h = V * ((c * W + wi) * 32 + lane);
-    const bool in = h < a.H;
+    for (int j = 0; j < RB; ++j) {
+      const size_t at = (size_t)(row + j) * a.H + h0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[c][i] = 0.f;
-    if (in) load_source<SRC, V>(a.x, a.from, r0 + h, v[c]);
-    if constexpr (SRC == kBf16 || SRC == kF32) {
-      if (a.y) {
-        if (in) {
-          float y[V];
-          load_rows<F32, V>(a.y, r0 + h, y);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[c][i] += y[i];
-          round_rows<F32, V>(v[c]);
-          store_rows<F32, V>(a.x_out, r0 + h, v[c]);
-        }
+      for (int c = 0; c < NC; ++c) {
+        clear(r[j][c]);
+        if (in[c] && (RB == 1 || row + j < a.T))
+          fetch_source<SRC, V>(r[j][c], a.x, a.from, at + 32 * V * c);
       }
-      if constexpr (V == 8) {
-        if (a.to.codes) {  // all lanes take part: H is a multiple of 32, so a block's four do
-          uint32_t byte;
-          const uint2 q = a.to.format == MXFP4_MOE_CHECKPOINT_E4M3 ? encode8<kE4m3>(v[c], byte)
-                                                                   : encode8<kInt8>(v[c], byte);
-          if (in) {
-            *reinterpret_cast<uint2*>(a.to.codes + r0 + h) = q;
-            if ((lane & 3) == 0) a.to.scales[(r0 + h) / 32] = (uint8_t)byte;
+    }
+    if (kRows && a.y) {
+      if constexpr (kRows) {
+        Raw<SRC, V> y[RB][NC];
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+          const size_t at = (size_t)(row + j) * a.H + h0;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            clear(y[j][c]);
+            if (in[c] && (RB == 1 || row + j < a.T)) fetch<SRC, V>(y[j][c], a.y, at + 32 * V * c);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+          const size_t at = (size_t)(row + j) * a.H + h0;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float f[V], u[V];
+            values<SRC, V>(r[j][c], f);
+            values<SRC, V>(y[j][c], u);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] += u[i];
+            into_raw<F32, V>(f, r[j][c]);
+            if (in[c] && (RB == 1 || row + j < a.T)) store_raw<F32, V>(a.x_out, at + 32 * V * c, r[j][c]);
           }
         }
       }
     }
-    if (!a.rms) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) part += v[c][i];
+    for (int j = 0; j < RB; ++j)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float f[V];
+        values<SRC, V>(r[j][c], f);
+        set<V>(v[j][c], f);
+      }
+  }
+  if constexpr (kRows && V == 8) {
+    if (a.to.codes) {
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          store_checkpoint(a.to, (size_t)(row + j) * a.H + h0 + 32 * V * c,
+                           in[c] && (RB == 1 || row + j < a.T), v[j][c]);
     }
   }
-  const float mean = a.rms ? 0.f : rg.sum(part, 0) / (float)a.H;
-  part = 0.f;
+  float mean[RB], rstd[RB];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int h = V * ((c * W + wi) * 32 + lane);
-    if (h < a.H) {
+  for (int j = 0; j < RB; ++j) {
+    mean[j] = 0.f;
+    if (!a.rms) {
+      Pair s;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        v[c][i] -= mean;
-        part += v[c][i] * v[c][i];
+      for (int c = 0; c < NC; ++c) add_sum<V>(s, v[j][c]);
+      mean[j] = group_sum(s.sum(), 0) * inv_h;
+    }
+    Pair s;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (in[c]) center<V>(s, v[j][c], mean[j]);
+    rstd[j] = rsqrtf(group_sum(s.sum(), 1) * inv_h + a.eps);
+    if (wi == 0 && lane == 0 && (RB == 1 || row + j < a.T)) {
+      if (a.mean) a.mean[row + j] = mean[j];
+      if (a.rstd) a.rstd[row + j] = rstd[j];
+    }
+  }
+  auto finish = [&](auto type) {  // parameters of either type, the branch outside the loops
+    constexpr int kP = decltype(type)::value;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (in[c]) {
+        float f[V];
+        Vals<V> g, b;
+        Raw<kP, V> rg, rb;
+        if (a.weight) fetch<kP, V>(rg, a.weight, h0 + 32 * V * c);
+        if (a.bias) fetch<kP, V>(rb, a.bias, h0 + 32 * V * c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = 1.f;
+        if (a.weight) values<kP, V>(rg, f);
+        set<V>(g, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = 0.f;
+        if (a.bias) values<kP, V>(rb, f);
+        set<V>(b, f);
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+          if (RB == 1 || row + j < a.T) {
+            scale_shift<V>(v[j][c], rstd[j], g, b);
+            get<V>(v[j][c], f);
+            store_rows<F32, V>(a.out, (size_t)(row + j) * a.H + h0 + 32 * V * c, f);
+          }
       }
     }
+  };
+  if (a.param_f32) finish(Index<kF32>{});
+  else finish(Index<kBf16>{});
+}
+
+// 16 (8) bytes to shared memory; with n == 0 nothing is read and zeros are written.  CA: by way
+// of L1, for the two halves of a 32-byte sector that two copies take.
+template <int DST, int SRC, bool CA>  // byte offsets known at compile time
+MOE_DEV void copy_async16(uint32_t dst, const void* src, uint32_t n) {
+  if constexpr (CA)
+    asm volatile("cp.async.ca.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(n), "n"(DST), "n"(SRC) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(n), "n"(DST), "n"(SRC) : "memory");
+}
+template <int DST, int SRC>
+MOE_DEV void copy_async8(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0 + %3], [%1 + %4], 8, %2;" ::"r"(dst), "l"(src),
+               "r"(n), "n"(DST), "n"(SRC) : "memory");
+}
+MOE_DEV void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N = 0>  // all but the N latest groups have arrived
+MOE_DEV void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// for_n<N>(f): f(integral_constant 0), ..., f(integral_constant N - 1)
+template <int N, int I = 0, class F>
+MOE_DEV void for_n(const F& f) {
+  if constexpr (I < N) {
+    f(Index<I>{});
+    for_n<N, I + 1>(f);
   }
-  const float rstd = 1.f / sqrtf(rg.sum(part, 1) / (float)a.H + a.eps);
-  if (wi == 0 && lane == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
+}
+
+// Totals of Q values over the W warps of a row group, in every lane: folded over each warp, then
+// one exchange through `buf` (W Q floats) behind the group's barrier.
+template <int Q>
+MOE_DEV void group_totals(float (&q)[Q], int W, int wi, int bar, float* buf) {
+  const int lane = threadIdx.x & 31;
+  float t = fold<Q>(q);
+  int step = 32 / Q;  // lanes between the totals of two values
+  if (W > 1) {
+    if ((lane & (step - 1)) == 0) buf[wi * Q + lane / step] = t;
+    group_barrier(bar, W);
+    t = lane < W * Q ? buf[lane] : 0.f;  // lane l holds value l % Q
+#pragma unroll
+    for (int i = 32; i < 16 * Q; i += 32) t += lane + i < W * Q ? buf[lane + i] : 0.f;
+#pragma unroll
+    for (int o = 16; o >= Q; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+    step = 1;
   }
+#pragma unroll
+  for (int i = 0; i < Q; ++i) q[i] = __shfl_sync(kFull, t, i * step);
+}
+
+// The form for many rows: persistent blocks whose groups of W warps take RB rows in turn.  A
+// lane copies the vectors that it will compute on into shared memory asynchronously (its own 16
+// bytes of each 512, so no lane waits for another), takes them into registers, and at once
+// requests the next rows' into the same place: the loads of a whole turn are in flight behind
+// the arithmetic of the one before, without registers for them.  A lane keeps the same features
+// throughout, so weight and bias stay in its registers; the RB rows share one folded reduction.
+template <int SRC> constexpr int kStage = SRC == kF32 ? 1024 : SRC == kBf16 ? 512 : 256;
+
+// A lane's vector from its place in a stage (fp32: two planes of 512 bytes).
+template <int SRC>
+MOE_DEV void read_stage(uint32_t from, Raw<SRC, 8>& r) {
+  if constexpr (SRC == kF32) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.a.x), "=f"(r.a.y), "=f"(r.a.z), "=f"(r.a.w) : "r"(from) : "memory");
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.b.x), "=f"(r.b.y), "=f"(r.b.z), "=f"(r.b.w) : "r"(from + 512) : "memory");
+  } else if constexpr (SRC == kBf16) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.q.x), "=r"(r.q.y), "=r"(r.q.z), "=r"(r.q.w) : "r"(from) : "memory");
+  } else {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.q.x), "=r"(r.q.y) : "r"(from) : "memory");
+  }
+}
+
+template <int SRC, bool F32, bool RES, int NC, int RB, int NT, int BLOCKS>
+__global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs a, int W) {
+  constexpr int V = 8;
+  constexpr bool kRows = SRC == kBf16 || SRC == kF32;
+  constexpr int kElem = SRC == kF32 ? 4 : SRC == kBf16 ? 2 : 1;  // bytes of a feature as read
+  constexpr int kOut = F32 ? 4 : 2;
+  constexpr int kTurn = RB * NC * kStage<SRC>;
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' stages
+  __shared__ float s_buf[NT / 32][2][2][RB * (NT / 32)];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
+  const int G = blockDim.x / (32 * W);
+  const uint32_t stage = smem_u32(s_dyn) + (uint32_t)warp * (RES ? 2 * kTurn : kTurn) +
+                         (kRows ? 16u : 8u) * lane;
+  const float inv_h = 1.f / (float)a.H;
+  const int h0 = V * (wi * NC * 32 + lane);  // the lane's vectors are 256 features apart
+  bool in[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) in[c] = h0 + 256 * c < a.H;
+  const int h0r = in[0] ? h0 : 0;
+  uint32_t byte[kRows ? 1 : RB][kRows ? 1 : NC];
+  // rows past the last one stand for it: they compute and store what it does
+  const uint32_t rows = (uint32_t)a.T;
+  auto offset = [&](uint32_t row, int j) { return (size_t)min(row + j, rows - 1) * (uint32_t)a.H + (uint32_t)h0r; };
+
+  auto request = [&](uint32_t row) {
+    for_n<RB>([&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      const size_t at = offset(row, j);
+      const uint8_t* x = kRows ? static_cast<const uint8_t*>(a.x) + at * kElem : a.from.codes + at;
+      const uint8_t* y = RES ? static_cast<const uint8_t*>(a.y) + at * kElem : nullptr;
+      for_n<NC>([&](auto cc) {
+        constexpr int c = decltype(cc)::value, to = (j * NC + c) * kStage<SRC>, from = 256 * c * kElem;
+        if constexpr (kRows) {
+          const uint32_t n = in[c] ? 16u : 0u;
+          copy_async16<to, from, SRC == kF32>(stage, x, n);
+          if constexpr (SRC == kF32) copy_async16<to + 512, from + 16, SRC == kF32>(stage, x, n);
+          if constexpr (RES) {
+            copy_async16<kTurn + to, from, SRC == kF32>(stage, y, n);
+            if constexpr (SRC == kF32) copy_async16<kTurn + to + 512, from + 16, SRC == kF32>(stage, y, n);
+          }
+        } else {
+          copy_async8<to, from>(stage, x, in[c] ? 8u : 0u);
+          byte[j][c] = __ldg(a.from.scales + (in[c] ? (at + 256 * c) / 32 : 0));
+        }
+      });
+    });
+    copy_async_commit();
+  };
+  const uint32_t step = gridDim.x * (uint32_t)(G * RB);
+  uint32_t row = (blockIdx.x * (uint32_t)G + group) * RB;
+  if (row < rows) request(row);
+  Vals<V> pg[NC], pb[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int h = V * ((c * W + wi) * 32 + lane);
-    if (h < a.H) {
-      float g[V], b[V];
-      load_params<V>(a.weight, a.param_f32, h, 1.f, g);
-      load_params<V>(a.bias, a.param_f32, h, 0.f, b);
+    float f[V];
+    load_params<V>(a.weight, a.param_f32, in[c] ? h0 + 256 * c : 0, 1.f, f);
+    set<V>(pg[c], f);
+    load_params<V>(a.bias, a.param_f32, in[c] ? h0 + 256 * c : 0, 0.f, f);
+    set<V>(pb[c], f);
+  }
+  int turn = 0;
+  for (; row < rows; row += step) {
+    Vals<V> v[RB][NC];
+    copy_async_wait<0>();
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[c][i] = fmaf(v[c][i] * rstd, g[i], b[i]);
-      store_rows<F32, V>(a.out, r0 + h, v[c]);
+    for (int j = 0; j < RB; ++j) {
+      uint8_t* x_out = RES ? static_cast<uint8_t*>(a.x_out) + offset(row, j) * kOut : nullptr;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const uint32_t from = stage + (uint32_t)(j * NC + c) * kStage<SRC>;
+        Raw<SRC, V> r;
+        float f[V];
+        read_stage<SRC>(from, r);
+        if constexpr (!kRows) r.byte = byte[j][c];
+        values<SRC, V>(r, f);
+        if constexpr (RES) {
+          float u[V];
+          read_stage<SRC>(from + kTurn, r);
+          values<SRC, V>(r, u);
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[i] += u[i];
+          into_raw<F32, V>(f, r);
+          if (in[c]) store_raw<F32, V>(x_out, 256 * c, r);
+          values<SRC, V>(r, f);
+        }
+        set<V>(v[j][c], f);
+      }
+    }
+    if (rows - row > step) request(row + step);  // this lane has read its places
+    if constexpr (kRows) {
+      if (a.to.codes) {
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            store_checkpoint(a.to, offset(row, j) + 256 * c, in[c], v[j][c]);
+      }
+    }
+    float mean[RB], q[RB];
+#pragma unroll
+    for (int j = 0; j < RB; ++j) mean[j] = 0.f;
+    if (!a.rms) {
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        Pair s;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) add_sum<V>(s, v[j][c]);
+        mean[j] = s.sum();
+      }
+      group_totals<RB>(mean, W, wi, 1 + group, s_buf[group][turn][0]);
+    }
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      mean[j] *= inv_h;
+      q[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        Pair s;
+        center<V>(s, v[j][c], mean[j]);
+        q[j] += in[c] ? s.sum() : 0.f;
+      }
+    }
+    group_totals<RB>(q, W, wi, 1 + group, s_buf[group][turn][1]);
+    turn ^= 1;  // the next rows' exchange must not meet this one's readers
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      q[j] = rsqrtf(q[j] * inv_h + a.eps);
+      if (wi == 0 && lane == 0) {
+        if (a.mean) a.mean[min(row + j, rows - 1)] = mean[j];
+        if (a.rstd) a.rstd[min(row + j, rows - 1)] = q[j];
+      }
+      uint8_t* out = static_cast<uint8_t*>(a.out) + offset(row, j) * kOut;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        scale_shift<V>(v[j][c], q[j], pg[c], pb[c]);
+        float f[V];
+        get<V>(v[j][c], f);
+        Row<F32, V> r;
+        into_raw<F32, V>(f, r);
+        if (in[c]) store_raw<F32, V>(out, 256 * c, r);
+      }
     }
   }
 }
 
 // ---- backward -------------------------------------------------------------------------------
-// A block walks over its share of the rows; a thread keeps the same features throughout, so the
-// parameters' gradients accumulate in its registers and leave once per block (a second kernel
-// adds the blocks' partial sums in a fixed order).
-constexpr int kParts = 296;  // most blocks, two per SM of a B200
+// A thread keeps the same features (V NC of them) over all rows of its block, so the parameters'
+// gradients accumulate in its registers and leave once per block; a second kernel adds the
+// blocks' partial sums in a fixed order.  R rows go at a time: their loads are in flight
+// together, and their 2 R sums (c1, c2 of each) are reduced over the warp in one folding pass
+// (2 R - 1 + the remaining halvings, in place of 5 shuffles each) and over the row's warps in
+// one exchange.
+constexpr int kParts = 296;  // most blocks: two per SM of a B200
 
-template <int SRC, bool F32, int V, int NC>
-__global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArgs a, int W,
-                                                                     int rows_per_block) {
-  __shared__ float s_buf[16][2][64];
-  __shared__ float s_sum[kNormThreads * V * NC / 2];
+// Where a block's sums of d_weight (0) or d_bias (1) go: its row of the partial sums, or the
+// gradient itself when there is no other block.
+MOE_DEV float* partial_row(const NormGradArgs& a, int which) {
+  if (gridDim.x == 1) return which ? a.d_bias : a.d_weight;
+  return a.partial + ((size_t)blockIdx.x * 2 + which) * a.H;
+}
+// The kernel that adds the partial sums is launched while this one ends, and waits for it.
+MOE_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+MOE_DEV void wait_for_launcher() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <int SRC, bool F32, int V, int NC, int R, bool HASG, int NT, int BLOCKS>
+__global__ void __launch_bounds__(NT, BLOCKS)
+    norm_backward_kernel(NormGradArgs a, int W, int rows_per_block) {
+  constexpr int Q = 2 * R;
+  constexpr bool kKeep = V * NC <= 16;  // registers for the weight, else read again (L1)
+  __shared__ float s_buf[NT / 32][2][16 * Q];
+  __shared__ float s_sum[V * NC * NT / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = blockDim.x / (32 * W), group = warp / W, wi = warp % W;
-  float acc_g[NC][V], acc_b[NC][V];
+  const int G = blockDim.x / (32 * W), group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
+  float acc_g[NC][V], acc_b[NC][V], kept[kKeep ? NC : 1][V];
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int c = 0; c < NC; ++c) {
+    const int h = feature<V>(c, W, wi, lane);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc_g[c][i] = acc_b[c][i] = 0.f;
-  const long long row_end = min((long long)a.T, (long long)(blockIdx.x + 1) * rows_per_block);
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) kept[c][i] = 0.f;
+      if (h < a.H) load_params<V>(a.weight, a.param_f32, h, 1.f, kept[c]);
+    }
+  }
+  auto weight = [&](int c, float (&w)[V]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = kept[c][i];
+    } else {
+      const int h = feature<V>(c, W, wi, lane);
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = 0.f;
+      if (h < a.H) load_params<V>(a.weight, a.param_f32, h, 1.f, w);
+    }
+  };
+  const float inv_h = 1.f / (float)a.H;
+  const long long begin = (long long)blockIdx.x * rows_per_block;
+  const long long end = min((long long)a.T, begin + rows_per_block);
   int turn = 0;
-  for (long long row = (long long)blockIdx.x * rows_per_block + group; row < row_end; row += G) {
-    const RowGroup rg{W, wi, 1 + group, s_buf[group][turn]};
-    turn ^= 1;  // the next row's exchange must not meet this one's readers
-    const size_t r0 = (size_t)row * a.H;
-    const float mean = a.rms ? 0.f : __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
-    float xh[NC][V], v[NC][V];
-    float c1 = 0.f, c2 = 0.f;
+  for (long long row = begin + (long long)group * R; row < end; row += (long long)G * R) {
+    Raw<SRC, V> x[R][NC];
+    Row<F32, V> d[R][NC], g[HASG ? R : 1][NC];
+    float mean[R], rstd[R];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int h = V * ((c * W + wi) * 32 + lane);
-      if (h < a.H) {
-        float d[V], g[V];
-        load_source<SRC, V>(a.x, a.from, r0 + h, xh[c]);
-        load_rows<F32, V>(a.d_out, r0 + h, d);
-        load_params<V>(a.weight, a.param_f32, h, 1.f, g);
+    for (int j = 0; j < R; ++j) {
+      const bool live = row + j < end;
+      const size_t r0 = (size_t)(row + j) * a.H;
+      mean[j] = live && !a.rms ? __ldg(a.mean + row + j) : 0.f;
+      rstd[j] = live ? __ldg(a.rstd + row + j) : 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          xh[c][i] = (xh[c][i] - mean) * rstd;
-          v[c][i] = d[i] * g[i];
-          c1 += v[c][i];
-          c2 += v[c][i] * xh[c][i];
-          acc_g[c][i] += d[i] * xh[c][i];
-          acc_b[c][i] += d[i];
+      for (int c = 0; c < NC; ++c) {
+        const int h = feature<V>(c, W, wi, lane);
+        const bool in = live && h < a.H;
+        clear(x[j][c]);
+        clear(d[j][c]);
+        if (in) {
+          fetch_source<SRC, V>(x[j][c], a.x, a.from, r0 + h);
+          fetch<F32 ? kF32 : kBf16, V>(d[j][c], a.d_out, r0 + h);
+          if constexpr (HASG) fetch_rw<F32 ? kF32 : kBf16, V>(g[j][c], a.g, r0 + h);
         }
       }
     }
-    c1 = a.rms ? 0.f : rg.sum(c1, 0) / (float)a.H;
-    c2 = rg.sum(c2, 1) / (float)a.H;
+    float q[Q];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int h = V * ((c * W + wi) * 32 + lane);
-      if (h < a.H) {
+    for (int j = 0; j < R; ++j) {
+      float c1 = 0.f, c2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[c][i] = rstd * (v[c][i] - c1 - xh[c][i] * c2);
-        if (a.g) {
-          float g[V];
-          load_rows<F32, V>(a.g, r0 + h, g);
+      for (int c = 0; c < NC; ++c) {
+        float xv[V], dv[V], pg[V];
+        values<SRC, V>(x[j][c], xv);
+        values<F32 ? kF32 : kBf16, V>(d[j][c], dv);
+        weight(c, pg);
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[c][i] += g[i];
+        for (int i = 0; i < V; ++i) {
+          const float xh = (xv[i] - mean[j]) * rstd[j];  // d = 0 past the row's end
+          const float v = dv[i] * pg[i];
+          c1 += v;
+          c2 = fmaf(v, xh, c2);
+          acc_g[c][i] = fmaf(dv[i], xh, acc_g[c][i]);
+          acc_b[c][i] += dv[i];
         }
-        store_rows<F32, V>(a.dx, r0 + h, v[c]);
+      }
+      q[2 * j] = c1;
+      q[2 * j + 1] = c2;
+    }
+    float total = fold<Q>(q);
+    int step = 32 / Q;  // lanes between the totals of two values
+    if (W > 1) {
+      float* buf = s_buf[group][turn];
+      turn ^= 1;  // the next rows' exchange must not meet this one's readers
+      if ((lane & (step - 1)) == 0) buf[wi * Q + lane / step] = total;
+      group_barrier(1 + group, W);
+      total = 0.f;
+      for (int i = lane; i < W * Q; i += 32) total += buf[i];
+#pragma unroll
+      for (int o = 16; o >= Q; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+      step = 1;
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const float c1 = a.rms ? 0.f : __shfl_sync(kFull, total, 2 * j * step) * inv_h;
+      const float c2 = __shfl_sync(kFull, total, (2 * j + 1) * step) * inv_h;
+      const size_t r0 = (size_t)(row + j) * a.H;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int h = feature<V>(c, W, wi, lane);
+        if (row + j < end && h < a.H) {
+          float xv[V], dv[V], pg[V];
+          values<SRC, V>(x[j][c], xv);
+          values<F32 ? kF32 : kBf16, V>(d[j][c], dv);
+          weight(c, pg);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float xh = (xv[i] - mean[j]) * rstd[j];
+            dv[i] = rstd[j] * (dv[i] * pg[i] - c1 - xh * c2);
+          }
+          if constexpr (HASG) {
+            float gv[V];
+            values<F32 ? kF32 : kBf16, V>(g[j][c], gv);
+#pragma unroll
+            for (int i = 0; i < V; ++i) dv[i] += gv[i];
+          }
+          store_rows<F32, V>(a.dx, r0 + h, dv);
+        }
       }
     }
   }
   if (!a.d_weight && !a.d_bias) return;
+  launch_dependents();
   // the block's sum over its groups, in group order, to its row of the partial sums
-  float* part = a.partial + (size_t)blockIdx.x * 2 * a.H;
+#pragma unroll
   for (int which = 0; which < 2; ++which) {
+    float* part = partial_row(a, which);
+    if (!part) continue;
     // groups other than the first pass theirs through shared memory one at a time
     for (int other = 1; other < G; ++other) {
       __syncthreads();
@@ -347,7 +887,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
         for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int i = 0; i < V; ++i)
-            s_sum[V * ((c * W + wi) * 32 + lane) + i] = which ? acc_b[c][i] : acc_g[c][i];
+            s_sum[feature<V>(c, W, wi, lane) + i] = which ? acc_b[c][i] : acc_g[c][i];
       }
       __syncthreads();
       if (group == 0) {
@@ -355,7 +895,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
         for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const float o = s_sum[V * ((c * W + wi) * 32 + lane) + i];
+            const float o = s_sum[feature<V>(c, W, wi, lane) + i];
             if (which) acc_b[c][i] += o; else acc_g[c][i] += o;
           }
       }
@@ -363,10 +903,213 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
     if (group == 0) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int h = V * ((c * W + wi) * 32 + lane);
+        const int h = feature<V>(c, W, wi, lane);
         if (h < a.H) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) part[which * a.H + h + i] = which ? acc_b[c][i] : acc_g[c][i];
+          for (int i = 0; i < V; ++i) part[h + i] = which ? acc_b[c][i] : acc_g[c][i];
+        }
+      }
+    }
+  }
+}
+
+// The staged form, for aligned rows of up to 8192 features: as the forward's persistent form,
+// the next rows of x and d_out travel into shared memory behind this turn's arithmetic (and
+// those of g behind the next turn's first half), a lane keeps its features' sums, and rows past
+// the block's last one read as zeros and store nothing.  x_hat and v stay in registers between
+// the sums and dx.
+template <int SRC, bool F32, bool HASG, int NC, int R, int NT, int BLOCKS>
+__global__ void __launch_bounds__(NT, BLOCKS)
+    norm_backward_staged_kernel(NormGradArgs a, int W, int rows_per_block) {
+  constexpr int V = 8, Q = 2 * R;
+  constexpr int kGrad = F32 ? kF32 : kBf16;
+  constexpr bool kRows = SRC == kBf16 || SRC == kF32;
+  constexpr int kX = kRows ? (SRC == kF32 ? 4 : 2) : 1, kD = F32 ? 4 : 2;  // bytes of a feature
+  constexpr int kXTurn = R * NC * kStage<SRC>, kDTurn = R * NC * kStage<kGrad>;
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // per warp: x, d_out, g
+  __shared__ float s_buf[NT / 32][2][Q * (NT / 32)];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
+  const int G = blockDim.x / (32 * W);
+  const uint32_t base = smem_u32(s_dyn) + (uint32_t)warp * (kXTurn + kDTurn + (HASG ? kDTurn : 0));
+  const uint32_t stage_x = base + (kRows ? 16u : 8u) * lane, stage_d = base + kXTurn + 16u * lane;
+  const float inv_h = 1.f / (float)a.H;
+  const int h0 = V * (wi * NC * 32 + lane);  // the lane's vectors are 256 features apart
+  bool in[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) in[c] = h0 + 256 * c < a.H;
+  const int h0r = in[0] ? h0 : 0;
+  Vals<V> acc_g[NC], acc_b[NC], pg[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = 0.f;
+    set<V>(acc_g[c], f);
+    set<V>(acc_b[c], f);
+    load_params<V>(a.weight, a.param_f32, in[c] ? h0 + 256 * c : 0, 1.f, f);
+    set<V>(pg[c], f);
+  }
+  const uint32_t begin = blockIdx.x * (uint32_t)rows_per_block;
+  const uint32_t end = min((uint32_t)a.T, begin + (uint32_t)rows_per_block);
+  auto offset = [&](uint32_t row, int j) { return (size_t)min(row + j, end - 1) * (uint32_t)a.H + (uint32_t)h0r; };
+  uint32_t byte[kRows ? 1 : R][kRows ? 1 : NC];
+  float mean_next[R], rstd_next[R];
+
+  auto request = [&](uint32_t row) {
+    for_n<R>([&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      const size_t at = offset(row, j);
+      const bool live = row + j < end;
+      const uint8_t* x = kRows ? static_cast<const uint8_t*>(a.x) + at * kX : a.from.codes + at;
+      const uint8_t* d = static_cast<const uint8_t*>(a.d_out) + at * kD;
+      for_n<NC>([&](auto cc) {
+        constexpr int c = decltype(cc)::value;
+        constexpr int tx = (j * NC + c) * kStage<SRC>, td = (j * NC + c) * kStage<kGrad>;
+        const uint32_t n = in[c] && live ? 16u : 0u;
+        if constexpr (kRows) {
+          copy_async16<tx, 256 * c * kX, SRC == kF32>(stage_x, x, n);
+          if constexpr (SRC == kF32) copy_async16<tx + 512, 256 * c * kX + 16, SRC == kF32>(stage_x, x, n);
+        } else {
+          copy_async8<tx, 256 * c>(stage_x, x, n / 2);
+          byte[j][c] = __ldg(a.from.scales + (in[c] ? (at + 256 * c) / 32 : 0));
+        }
+        copy_async16<td, 256 * c * kD, F32>(stage_d, d, n);
+        if constexpr (F32) copy_async16<td + 512, 256 * c * kD + 16, F32>(stage_d, d, n);
+      });
+      const uint32_t r = min(row + j, end - 1);
+      mean_next[j] = a.rms ? 0.f : __ldg(a.mean + r);
+      rstd_next[j] = live ? __ldg(a.rstd + r) : 0.f;
+    });
+    copy_async_commit();
+  };
+  auto request_g = [&](uint32_t row) {
+    for_n<R>([&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      const uint8_t* g = static_cast<const uint8_t*>(a.g) + offset(row, j) * kD;
+      for_n<NC>([&](auto cc) {
+        constexpr int c = decltype(cc)::value, td = kDTurn + (j * NC + c) * kStage<kGrad>;
+        const uint32_t n = in[c] && row + j < end ? 16u : 0u;
+        copy_async16<td, 256 * c * kD, F32>(stage_d, g, n);
+        if constexpr (F32) copy_async16<td + 512, 256 * c * kD + 16, F32>(stage_d, g, n);
+      });
+    });
+    copy_async_commit();
+  };
+
+  const uint32_t step = (uint32_t)(G * R);
+  uint32_t row = begin + (uint32_t)(group * R);
+  if (row < end) {
+    request(row);
+    if constexpr (HASG) request_g(row);
+  }
+  int turn = 0;
+  for (; row < end; row += step) {
+    if constexpr (HASG) copy_async_wait<1>(); else copy_async_wait<0>();  // x and d_out
+    Vals<V> xh[R][NC], v[R][NC];
+    float q[Q], rstd[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      rstd[j] = rstd_next[j];
+      const uint64_t m2 = f2(-mean_next[j], -mean_next[j]), r2 = f2(rstd[j], rstd[j]);
+      Pair c1, c2;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        Raw<SRC, V> rx;
+        Raw<kGrad, V> rd;
+        read_stage<SRC>(stage_x + (uint32_t)(j * NC + c) * kStage<SRC>, rx);
+        read_stage<kGrad>(stage_d + (uint32_t)(j * NC + c) * kStage<kGrad>, rd);
+        if constexpr (!kRows) rx.byte = byte[j][c];
+        float f[V];
+        values<SRC, V>(rx, f);
+        set<V>(xh[j][c], f);
+        values<kGrad, V>(rd, f);
+        set<V>(v[j][c], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          xh[j][c].p[i] = f2mul(f2add(xh[j][c].p[i], m2), r2);
+          const uint64_t d = v[j][c].p[i];
+          acc_g[c].p[i] = f2fma(d, xh[j][c].p[i], acc_g[c].p[i]);
+          acc_b[c].p[i] = f2add(acc_b[c].p[i], d);
+          v[j][c].p[i] = f2mul(d, pg[c].p[i]);
+          c1.p = f2add(c1.p, v[j][c].p[i]);
+          c2.p = f2fma(v[j][c].p[i], xh[j][c].p[i], c2.p);
+        }
+      }
+      q[2 * j] = a.rms ? 0.f : c1.sum();
+      q[2 * j + 1] = c2.sum();
+    }
+    const bool more = end - row > step;
+    if (more) request(row + step);  // this lane has read its places
+    group_totals<Q>(q, W, wi, 1 + group, s_buf[group][turn]);
+    turn ^= 1;  // the next rows' exchange must not meet this one's readers
+    if constexpr (HASG) {
+      if (more) copy_async_wait<1>(); else copy_async_wait<0>();  // g
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const float k1 = -rstd[j] * (q[2 * j] * inv_h), k2 = -rstd[j] * (q[2 * j + 1] * inv_h);
+      const uint64_t p1 = f2(k1, k1), p2 = f2(k2, k2), r2 = f2(rstd[j], rstd[j]);
+      uint8_t* dx = static_cast<uint8_t*>(a.dx) + offset(row, j) * kD;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[j][c].p[i] = f2fma(v[j][c].p[i], r2, f2fma(xh[j][c].p[i], p2, p1));
+        float f[V];
+        Row<F32, V> r;
+        if constexpr (HASG) {
+          read_stage<kGrad>(stage_d + kDTurn + (uint32_t)(j * NC + c) * kStage<kGrad>, r);
+          Vals<V> g;
+          values<kGrad, V>(r, f);
+          set<V>(g, f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][c].p[i] = f2add(v[j][c].p[i], g.p[i]);
+        }
+        get<V>(v[j][c], f);
+        into_raw<F32, V>(f, r);
+        if (in[c] && row + j < end) store_raw<F32, V>(dx, 256 * c, r);
+      }
+    }
+    if constexpr (HASG) {
+      if (more) request_g(row + step);
+    }
+  }
+  if (!a.d_weight && !a.d_bias) return;
+  launch_dependents();
+  // the block's sum over its groups, in group order, to its row of the partial sums
+  __syncthreads();
+  float* s_sum = reinterpret_cast<float*>(s_dyn);  // the groups' sums of one kind, 32 V NC W each
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float* part = partial_row(a, which);
+    if (!part) continue;
+    const Vals<V>* acc = which ? acc_b : acc_g;
+    if (G > 1) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float f[V];
+        get<V>(acc[c], f);
+        float4* to = reinterpret_cast<float4*>(s_sum + (size_t)group * 256 * NC * W + h0 + 256 * c);
+        to[0] = make_float4(f[0], f[1], f[2], f[3]);
+        to[1] = make_float4(f[4], f[5], f[6], f[7]);
+      }
+      __syncthreads();
+      for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
+        float t = 0.f;
+        for (int g = 0; g < G; ++g) t += s_sum[(size_t)g * 256 * NC * W + h];
+        part[h] = t;
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float f[V];
+        get<V>(acc[c], f);
+        if (in[c]) {
+          float4* to = reinterpret_cast<float4*>(part + h0 + 256 * c);
+          to[0] = make_float4(f[0], f[1], f[2], f[3]);
+          to[1] = make_float4(f[4], f[5], f[6], f[7]);
         }
       }
     }
@@ -374,24 +1117,28 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
 }
 
 // d_weight (blockIdx.y 0) and d_bias (1) from the blocks' partial sums: 32 features per block,
-// eight warps over the parts.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restrict__ partial,
-                                                          int parts, int H,
-                                                          float* __restrict__ d_weight,
-                                                          float* __restrict__ d_bias) {
-  __shared__ float s[8][33];
+// its warps over the parts.
+constexpr int kReduceWarps = 16;
+__global__ void __launch_bounds__(32 * kReduceWarps) norm_reduce_kernel(
+    const float* __restrict__ partial, int parts, int H, float* __restrict__ d_weight,
+    float* __restrict__ d_bias) {
+  __shared__ float s[kReduceWarps][33];
   float* out = blockIdx.y ? d_bias : d_weight;
-  if (!out) return;
+  if (!out) return;  // uniform in the block
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (h < H)
-    for (int p = warp; p < parts; p += 8) v += partial[((size_t)p * 2 + blockIdx.y) * H + h];
+  wait_for_launcher();
+  if (h < H) {
+    const float* p = partial + (size_t)blockIdx.y * H + h;
+#pragma unroll 8
+    for (int i = warp; i < parts; i += kReduceWarps) v += p[(size_t)i * 2 * H];
+  }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && h < H) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][lane];
+    for (int i = 1; i < kReduceWarps; ++i) v += s[i][lane];
     out[h] = v;
   }
 }
@@ -402,8 +1149,11 @@ __global__ void __launch_bounds__(256) checkpoint_pack_kernel(const void* x, lon
                                                               mxfp4_moe_checkpoint to) {
   const long long c = (long long)blockIdx.x * 256 + threadIdx.x;
   const bool in = c < chunks;  // whole blocks of four lanes
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (in) load_rows<F32, 8>(x, (size_t)c * 8, v);
+  Row<F32, 8> r;
+  clear(r);
+  if (in) fetch<F32 ? kF32 : kBf16, 8>(r, x, (size_t)c * 8);
+  float v[8];
+  values<F32 ? kF32 : kBf16, 8>(r, v);
   uint32_t byte;
   const uint2 q = encode8<FMT>(v, byte);
   if (in) {
@@ -424,72 +1174,135 @@ __global__ void __launch_bounds__(256) checkpoint_unpack_kernel(mxfp4_moe_checkp
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Features a thread holds, and the warps that hold a row, for rows of H features in vectors of V.
-struct Split {
-  int per_thread, W;
+// Rows of a batch from which the forward takes its persistent form.
+constexpr int kManyRows = 600;
+
+template <int SRC, bool F32, bool RES, int NC, int RB, int NT, int BLOCKS>
+cudaError_t forward_persistent(const NormArgs& a, int W, int sms, cudaStream_t st) {
+  auto kern = norm_forward_many_kernel<SRC, F32, RES, NC, RB, NT, BLOCKS>;
+  const int groups = NT / (32 * W);
+  const int smem = W * groups * RB * NC * kStage<SRC> * (RES ? 2 : 1);  // at most 128 KB
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * W * groups, smem);
+  if (e != cudaSuccess) return e;
+  const long long need = ((long long)a.T + RB * groups - 1) / (RB * groups);
+  const long long most = (long long)sms * (per_sm > 0 ? per_sm : 1);
+  kern<<<(unsigned)(need < most ? need : most), 32 * W * groups, smem, st>>>(a, W);
+  return cudaGetLastError();
+}
+template <int SRC, bool F32, int NC, int RB, int NT, int BLOCKS>
+cudaError_t forward_many(const NormArgs& a, int W, int sms, cudaStream_t st) {
+  if constexpr (SRC == kBf16 || SRC == kF32)
+    if (a.y) return forward_persistent<SRC, F32, true, NC, RB, NT, BLOCKS>(a, W, sms, st);
+  return forward_persistent<SRC, F32, false, NC, RB, NT, BLOCKS>(a, W, sms, st);
+}
+template <int SRC, bool F32, int V, int NC, int RB>
+cudaError_t forward_launch(const NormArgs& a, int W, cudaStream_t st) {
+  const int groups = W >= 4 ? 1 : 4 / W;
+  norm_forward_kernel<SRC, F32, V, NC, RB>
+      <<<(unsigned)(((long long)a.T + RB * groups - 1) / (RB * groups)), 32 * W * groups, 0, st>>>(a, W);
+  return cudaGetLastError();
+}
+
+template <int SRC, bool F32>
+cudaError_t forward_from(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
+  if (vec) {
+    const int units = a.H / 8;
+    auto warps = [&](int nc) { return (units + 32 * nc - 1) / (32 * nc); };
+    if (a.T >= kManyRows) {
+      if (units <= 384) return forward_many<SRC, F32, 1, 4, 384, 2>(a, warps(1), sms, st);
+      if (units <= 512) return forward_many<SRC, F32, 1, 2, 512, 2>(a, warps(1), sms, st);
+      if (units <= 1024) return forward_many<SRC, F32, 2, 2, 512, 1>(a, warps(2), sms, st);
+      return forward_many<SRC, F32, 4, 1, 512, 1>(a, warps(4), sms, st);
+    }
+    if (units <= 512) return forward_launch<SRC, F32, 8, 1, 1>(a, warps(1), st);
+    if (units <= 1024) return forward_launch<SRC, F32, 8, 2, 1>(a, warps(2), st);
+    return forward_launch<SRC, F32, 8, 4, 1>(a, warps(4), st);
+  }
+  if constexpr (SRC == kBf16 || SRC == kF32) {
+    if (a.H <= 4096) return forward_launch<SRC, F32, 1, 8, 1>(a, (a.H + 255) / 256, st);
+    return forward_launch<SRC, F32, 1, 32, 1>(a, (a.H + 1023) / 1024, st);
+  }
+  return cudaErrorInvalidValue;  // checkpoints are aligned
+}
+
+// Rows that a block of the backward walks over, and the blocks of a batch of T: as many as run at
+// once (a block's partial sums cost a row of fp32 and its part of the second kernel).
+struct Share {
+  int rows, blocks;
 };
-Split split_row(int H, int V, int most_warps) {
-  const int units = (H + V - 1) / V;
-  for (int nc = 8 / V; nc < 32 / V; nc *= 2) {
-    const int W = (units + 32 * nc - 1) / (32 * nc);
-    if (W <= most_warps) return {nc * V, W};
-  }
-  return {32, (units * V + 1023) / 1024};
+Share share_rows(int T, int step, int per_sm) {
+  const int most = kParts / 2 * per_sm;
+  if (T <= step) return {T, 1};
+  long long rows = ((long long)T + most - 1) / most;
+  if (rows > step) rows = (rows + step - 1) / step * step;
+  return {(int)rows, (int)((T + rows - 1) / rows)};
 }
 
-template <int SRC, bool F32>
-cudaError_t forward_from(const NormArgs& a, bool vec, cudaStream_t st) {
-  const Split s = split_row(a.H, vec ? 8 : 1, 4);
-  const int groups = s.W >= 8 ? 1 : 8 / s.W;
-  const unsigned blocks = (unsigned)(((long long)a.T + groups - 1) / groups);
-  const int threads = 32 * s.W * groups;
-  if (vec) {
-    if (s.per_thread == 8) norm_forward_kernel<SRC, F32, 8, 1><<<blocks, threads, 0, st>>>(a, s.W);
-    else if (s.per_thread == 16) norm_forward_kernel<SRC, F32, 8, 2><<<blocks, threads, 0, st>>>(a, s.W);
-    else norm_forward_kernel<SRC, F32, 8, 4><<<blocks, threads, 0, st>>>(a, s.W);
-  } else if constexpr (SRC == kBf16 || SRC == kF32) {
-    if (s.per_thread == 8) norm_forward_kernel<SRC, F32, 1, 8><<<blocks, threads, 0, st>>>(a, s.W);
-    else if (s.per_thread == 16) norm_forward_kernel<SRC, F32, 1, 16><<<blocks, threads, 0, st>>>(a, s.W);
-    else norm_forward_kernel<SRC, F32, 1, 32><<<blocks, threads, 0, st>>>(a, s.W);
-  } else {
-    return cudaErrorInvalidValue;
-  }
+template <int SRC, bool F32, int V, int NC, int R, bool HASG, int NT, int BLOCKS>
+cudaError_t backward_launch(const NormGradArgs& a, int W, int* parts, cudaStream_t st) {
+  const int groups = NT / (32 * W) > 0 ? NT / (32 * W) : 1;
+  const Share sh = share_rows(a.T, R * groups, BLOCKS);
+  *parts = sh.blocks;
+  norm_backward_kernel<SRC, F32, V, NC, R, HASG, NT, BLOCKS>
+      <<<sh.blocks, 32 * W * groups, 0, st>>>(a, W, sh.rows);
   return cudaGetLastError();
 }
 
-template <int SRC, bool F32>
-cudaError_t backward_from(const NormGradArgs& a, bool vec, cudaStream_t st) {
-  const Split s = split_row(a.H, vec ? 8 : 1, 16);
-  const int groups = s.W >= 8 ? 1 : 8 / s.W;
-  const int threads = 32 * s.W * groups;
-  const int rows = (int)(((long long)a.T + kParts - 1) / kParts);
-  const unsigned blocks = (unsigned)((a.T + (long long)rows - 1) / rows);
-  if (vec) {
-    if (s.per_thread == 8) norm_backward_kernel<SRC, F32, 8, 1><<<blocks, threads, 0, st>>>(a, s.W, rows);
-    else if (s.per_thread == 16) norm_backward_kernel<SRC, F32, 8, 2><<<blocks, threads, 0, st>>>(a, s.W, rows);
-    else norm_backward_kernel<SRC, F32, 8, 4><<<blocks, threads, 0, st>>>(a, s.W, rows);
-  } else if constexpr (SRC == kBf16 || SRC == kF32) {
-    if (s.per_thread == 8) norm_backward_kernel<SRC, F32, 1, 8><<<blocks, threads, 0, st>>>(a, s.W, rows);
-    else if (s.per_thread == 16) norm_backward_kernel<SRC, F32, 1, 16><<<blocks, threads, 0, st>>>(a, s.W, rows);
-    else norm_backward_kernel<SRC, F32, 1, 32><<<blocks, threads, 0, st>>>(a, s.W, rows);
-  } else {
-    return cudaErrorInvalidValue;
-  }
+template <int SRC, bool F32, bool HASG, int NC, int R, int NT, int BLOCKS>
+cudaError_t backward_staged(const NormGradArgs& a, int W, int* parts, cudaStream_t st) {
+  auto kern = norm_backward_staged_kernel<SRC, F32, HASG, NC, R, NT, BLOCKS>;
+  constexpr int kGrad = F32 ? kF32 : kBf16;
+  const int groups = NT / (32 * W);
+  int smem = W * groups * R * NC * (kStage<SRC> + kStage<kGrad> * (HASG ? 2 : 1));
+  const int sums = 4 * 256 * NC * W * groups;  // the groups' sums at the end
+  if (smem < sums) smem = sums;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const Share sh = share_rows(a.T, R * groups, BLOCKS);
+  *parts = sh.blocks;
+  kern<<<sh.blocks, 32 * W * groups, smem, st>>>(a, W, sh.rows);
   return cudaGetLastError();
+}
+
+template <int SRC, bool F32, bool HASG>
+cudaError_t backward_from(const NormGradArgs& a, bool vec, int* parts, cudaStream_t st) {
+  if (vec) {
+    const int W1 = (a.H + 255) / 256, W2 = (a.H + 511) / 512;
+    if (W1 <= 12) return backward_staged<SRC, F32, HASG, 1, 2, 384, 2>(a, W1, parts, st);
+    if (W1 <= 16) return backward_staged<SRC, F32, HASG, 1, F32 ? 2 : 4, 512, 1>(a, W1, parts, st);
+    if (W2 <= 16) return backward_staged<SRC, F32, HASG, 2, 1, 512, 1>(a, W2, parts, st);
+    return backward_launch<SRC, F32, 8, 4, 1, HASG, 512, 1>(a, (a.H + 1023) / 1024, parts, st);
+  }
+  if constexpr (SRC == kBf16 || SRC == kF32) {
+    const int W8 = (a.H + 255) / 256, W16 = (a.H + 511) / 512;
+    if (W8 <= 12) return backward_launch<SRC, F32, 1, 8, 1, HASG, 384, 2>(a, W8, parts, st);
+    if (W16 <= 16) return backward_launch<SRC, F32, 1, 16, 1, HASG, 512, 1>(a, W16, parts, st);
+    return backward_launch<SRC, F32, 1, 32, 1, HASG, 512, 1>(a, (a.H + 1023) / 1024, parts, st);
+  }
+  return cudaErrorInvalidValue;  // checkpoints are aligned
+}
+
+template <int SRC, bool F32>
+cudaError_t backward_pick(const NormGradArgs& a, bool vec, int* parts, cudaStream_t st) {
+  return a.g ? backward_from<SRC, F32, true>(a, vec, parts, st)
+             : backward_from<SRC, F32, false>(a, vec, parts, st);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_forward(const NormArgs& a, int, cudaStream_t st) {
+cudaError_t launch_norm_forward(const NormArgs& a, int sms, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
   const bool vec = a.H % 8 == 0 && al16(a.x) && al16(a.y) && al16(a.x_out) && al16(a.out) &&
                    al16(a.weight) && al16(a.bias);
   if (a.from.codes) {
     if (a.from.format == MXFP4_MOE_CHECKPOINT_E4M3)
-      return a.rows_f32 ? forward_from<kE4m3, true>(a, vec, st) : forward_from<kE4m3, false>(a, vec, st);
-    return a.rows_f32 ? forward_from<kInt8, true>(a, vec, st) : forward_from<kInt8, false>(a, vec, st);
+      return a.rows_f32 ? forward_from<kE4m3, true>(a, vec, sms, st) : forward_from<kE4m3, false>(a, vec, sms, st);
+    return a.rows_f32 ? forward_from<kInt8, true>(a, vec, sms, st) : forward_from<kInt8, false>(a, vec, sms, st);
   }
-  return a.rows_f32 ? forward_from<kF32, true>(a, vec, st) : forward_from<kBf16, false>(a, vec, st);
+  return a.rows_f32 ? forward_from<kF32, true>(a, vec, sms, st) : forward_from<kBf16, false>(a, vec, sms, st);
 }
 
 size_t norm_scratch_bytes(int T, int H) {
@@ -502,20 +1315,30 @@ cudaError_t launch_norm_backward(const NormGradArgs& a, int, cudaStream_t st) {
     const bool vec = a.H % 8 == 0 && al16(a.x) && al16(a.d_out) && al16(a.g) && al16(a.dx) &&
                      al16(a.weight);
     cudaError_t e;
-    if (a.from.codes)
-      e = a.from.format == MXFP4_MOE_CHECKPOINT_E4M3
-              ? (a.rows_f32 ? backward_from<kE4m3, true>(a, vec, st) : backward_from<kE4m3, false>(a, vec, st))
-              : (a.rows_f32 ? backward_from<kInt8, true>(a, vec, st) : backward_from<kInt8, false>(a, vec, st));
+    if (a.from.codes && a.from.format == MXFP4_MOE_CHECKPOINT_E4M3)
+      e = a.rows_f32 ? backward_pick<kE4m3, true>(a, vec, &parts, st)
+                     : backward_pick<kE4m3, false>(a, vec, &parts, st);
+    else if (a.from.codes)
+      e = a.rows_f32 ? backward_pick<kInt8, true>(a, vec, &parts, st)
+                     : backward_pick<kInt8, false>(a, vec, &parts, st);
     else
-      e = a.rows_f32 ? backward_from<kF32, true>(a, vec, st) : backward_from<kBf16, false>(a, vec, st);
+      e = a.rows_f32 ? backward_pick<kF32, true>(a, vec, &parts, st)
+                     : backward_pick<kBf16, false>(a, vec, &parts, st);
     if (e != cudaSuccess) return e;
-    const int rows = (int)(((long long)a.T + kParts - 1) / kParts);
-    parts = (a.T + rows - 1) / rows;
   }
   if (!a.d_weight && !a.d_bias) return cudaSuccess;
-  norm_reduce_kernel<<<dim3((a.H + 31) / 32, 2), 256, 0, st>>>(a.partial, parts, a.H, a.d_weight,
-                                                              a.d_bias);
-  return cudaGetLastError();
+  if (parts == 1) return cudaSuccess;  // one block writes the gradients itself
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.H + 31) / 32, 2);
+  cfg.blockDim = dim3(32 * kReduceWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = parts > 0 ? 1 : 0;  // T = 0: no kernel to overlap
+  return cudaLaunchKernelEx(&cfg, norm_reduce_kernel, (const float*)a.partial, parts, a.H,
+                            a.d_weight, a.d_bias);
 }
 
 cudaError_t launch_checkpoint_pack(int T, int H, bool rows_f32, const void* x,

@@ -19,7 +19,7 @@ struct RouteArgs {
   int groups, gsize, top_groups;
   uint32_t gmagic;   // e / gsize = e * gmagic >> 16 for e < 256
   bool sigmoid, best2, renorm;
-  float scale;
+  float scale, inv_scale;
   const float* logits;
   const float* bias;
   int32_t* idx;
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(
       for (int i = 0; i < NG; ++i) out[i] = c * l[i];
     }
   }
-  const float shared = a.renorm ? dot / a.scale : 0.f;
+  const float shared = a.renorm ? dot * a.inv_scale : 0.f;
   for (int j0 = 0; j0 < a.k; j0 += 32) {
     const int j = j0 + lane;
     int e = -1;
@@ -434,6 +434,7 @@ RouteArgs route_args(const mxfp4_moe_routing& r) {
   a.best2 = r.group_best == 2;
   a.renorm = r.renormalize != 0;
   a.scale = r.scale;
+  a.inv_scale = 1.f / r.scale;
   return a;
 }
 
