@@ -16,6 +16,10 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 // Where a pass reads its rows from.
 enum Source : int { kBf16 = 0, kF32 = 1, kE4m3 = 2, kInt8 = 3 };
 
+// The warp's index as a value that is the same in all its lanes for the compiler too, so that row
+// numbers and row addresses are computed once per warp.
+MOE_DEV int warp_index() { return __shfl_sync(kFull, (int)threadIdx.x >> 5, 0); }
+
 MOE_DEV float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -371,7 +375,7 @@ template <int I> struct Index { static constexpr int value = I; };
 template <int SRC, bool F32, int V, int NC, int RB>
 __global__ void __launch_bounds__(512) norm_forward_kernel(NormArgs a, int W) {
   __shared__ __align__(16) float s_buf[2][16][16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
   const long long row = ((long long)blockIdx.x * (blockDim.x / (32 * W)) + group) * RB;
   if (row >= a.T) return;  // whole groups leave together
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
   constexpr int kTurn = RB * NC * kStage<SRC>;
   extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' stages
   __shared__ float s_buf[NT / 32][2][2][RB * (NT / 32)];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
   const int G = blockDim.x / (32 * W);
   const uint32_t stage = smem_u32(s_dyn) + (uint32_t)warp * (RES ? 2 * kTurn : kTurn) +
@@ -606,14 +610,14 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
   uint32_t byte[kRows ? 1 : RB][kRows ? 1 : NC];
   // rows past the last one stand for it: they compute and store what it does
   const uint32_t rows = (uint32_t)a.T;
-  auto offset = [&](uint32_t row, int j) { return (size_t)min(row + j, rows - 1) * (uint32_t)a.H + (uint32_t)h0r; };
+  auto offset = [&](uint32_t row, int j) { return (size_t)min(row + j, rows - 1) * (uint32_t)a.H; };
 
   auto request = [&](uint32_t row) {
     for_n<RB>([&](auto jj) {
       constexpr int j = decltype(jj)::value;
       const size_t at = offset(row, j);
-      const uint8_t* x = kRows ? static_cast<const uint8_t*>(a.x) + at * kElem : a.from.codes + at;
-      const uint8_t* y = RES ? static_cast<const uint8_t*>(a.y) + at * kElem : nullptr;
+      const uint8_t* x = (kRows ? static_cast<const uint8_t*>(a.x) + at * kElem : a.from.codes + at) + h0r * kElem;
+      const uint8_t* y = RES ? static_cast<const uint8_t*>(a.y) + at * kElem + h0r * kElem : nullptr;
       for_n<NC>([&](auto cc) {
         constexpr int c = decltype(cc)::value, to = (j * NC + c) * kStage<SRC>, from = 256 * c * kElem;
         if constexpr (kRows) {
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
           }
         } else {
           copy_async8<to, from>(stage, x, in[c] ? 8u : 0u);
-          byte[j][c] = __ldg(a.from.scales + (in[c] ? (at + 256 * c) / 32 : 0));
+          byte[j][c] = __ldg(a.from.scales + at / 32 + (in[c] ? h0 / 32 + 8 * c : 0));
         }
       });
     });
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
     copy_async_wait<0>();
 #pragma unroll
     for (int j = 0; j < RB; ++j) {
-      uint8_t* x_out = RES ? static_cast<uint8_t*>(a.x_out) + offset(row, j) * kOut : nullptr;
+      uint8_t* x_out = RES ? static_cast<uint8_t*>(a.x_out) + offset(row, j) * kOut + h0 * kOut : nullptr;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const uint32_t from = stage + (uint32_t)(j * NC + c) * kStage<SRC>;
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
         for (int j = 0; j < RB; ++j)
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            store_checkpoint(a.to, offset(row, j) + 256 * c, in[c], v[j][c]);
+            store_checkpoint(a.to, offset(row, j) + h0 + 256 * c, in[c], v[j][c]);
       }
     }
     float mean[RB], q[RB];
@@ -715,7 +719,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
         if (a.mean) a.mean[min(row + j, rows - 1)] = mean[j];
         if (a.rstd) a.rstd[min(row + j, rows - 1)] = q[j];
       }
-      uint8_t* out = static_cast<uint8_t*>(a.out) + offset(row, j) * kOut;
+      uint8_t* out = static_cast<uint8_t*>(a.out) + offset(row, j) * kOut + h0 * kOut;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         scale_shift<V>(v[j][c], q[j], pg[c], pb[c]);
@@ -755,7 +759,7 @@ __global__ void __launch_bounds__(NT, BLOCKS)
   constexpr bool kKeep = V * NC <= 16;  // registers for the weight, else read again (L1)
   __shared__ float s_buf[NT / 32][2][16 * Q];
   __shared__ float s_sum[V * NC * NT / 2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int G = blockDim.x / (32 * W), group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
   float acc_g[NC][V], acc_b[NC][V], kept[kKeep ? NC : 1][V];
 #pragma unroll
@@ -928,7 +932,7 @@ __global__ void __launch_bounds__(NT, BLOCKS)
   constexpr int kXTurn = R * NC * kStage<SRC>, kDTurn = R * NC * kStage<kGrad>;
   extern __shared__ __align__(16) uint8_t s_dyn[];  // per warp: x, d_out, g
   __shared__ float s_buf[NT / 32][2][Q * (NT / 32)];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
   const int G = blockDim.x / (32 * W);
   const uint32_t base = smem_u32(s_dyn) + (uint32_t)warp * (kXTurn + kDTurn + (HASG ? kDTurn : 0));
@@ -952,7 +956,7 @@ __global__ void __launch_bounds__(NT, BLOCKS)
   }
   const uint32_t begin = blockIdx.x * (uint32_t)rows_per_block;
   const uint32_t end = min((uint32_t)a.T, begin + (uint32_t)rows_per_block);
-  auto offset = [&](uint32_t row, int j) { return (size_t)min(row + j, end - 1) * (uint32_t)a.H + (uint32_t)h0r; };
+  auto offset = [&](uint32_t row, int j) { return (size_t)min(row + j, end - 1) * (uint32_t)a.H; };
   uint32_t byte[kRows ? 1 : R][kRows ? 1 : NC];
   float mean_next[R], rstd_next[R];
 
@@ -961,8 +965,8 @@ __global__ void __launch_bounds__(NT, BLOCKS)
       constexpr int j = decltype(jj)::value;
       const size_t at = offset(row, j);
       const bool live = row + j < end;
-      const uint8_t* x = kRows ? static_cast<const uint8_t*>(a.x) + at * kX : a.from.codes + at;
-      const uint8_t* d = static_cast<const uint8_t*>(a.d_out) + at * kD;
+      const uint8_t* x = (kRows ? static_cast<const uint8_t*>(a.x) + at * kX : a.from.codes + at) + h0r * kX;
+      const uint8_t* d = static_cast<const uint8_t*>(a.d_out) + at * kD + h0r * kD;
       for_n<NC>([&](auto cc) {
         constexpr int c = decltype(cc)::value;
         constexpr int tx = (j * NC + c) * kStage<SRC>, td = (j * NC + c) * kStage<kGrad>;
@@ -972,7 +976,7 @@ __global__ void __launch_bounds__(NT, BLOCKS)
           if constexpr (SRC == kF32) copy_async16<tx + 512, 256 * c * kX + 16, SRC == kF32>(stage_x, x, n);
         } else {
           copy_async8<tx, 256 * c>(stage_x, x, n / 2);
-          byte[j][c] = __ldg(a.from.scales + (in[c] ? (at + 256 * c) / 32 : 0));
+          byte[j][c] = __ldg(a.from.scales + at / 32 + (in[c] ? h0 / 32 + 8 * c : 0));
         }
         copy_async16<td, 256 * c * kD, F32>(stage_d, d, n);
         if constexpr (F32) copy_async16<td + 512, 256 * c * kD + 16, F32>(stage_d, d, n);
@@ -986,7 +990,7 @@ __global__ void __launch_bounds__(NT, BLOCKS)
   auto request_g = [&](uint32_t row) {
     for_n<R>([&](auto jj) {
       constexpr int j = decltype(jj)::value;
-      const uint8_t* g = static_cast<const uint8_t*>(a.g) + offset(row, j) * kD;
+      const uint8_t* g = static_cast<const uint8_t*>(a.g) + offset(row, j) * kD + h0r * kD;
       for_n<NC>([&](auto cc) {
         constexpr int c = decltype(cc)::value, td = kDTurn + (j * NC + c) * kStage<kGrad>;
         const uint32_t n = in[c] && row + j < end ? 16u : 0u;
@@ -1050,7 +1054,7 @@ __global__ void __launch_bounds__(NT, BLOCKS)
     for (int j = 0; j < R; ++j) {
       const float k1 = -rstd[j] * (q[2 * j] * inv_h), k2 = -rstd[j] * (q[2 * j + 1] * inv_h);
       const uint64_t p1 = f2(k1, k1), p2 = f2(k2, k2), r2 = f2(rstd[j], rstd[j]);
-      uint8_t* dx = static_cast<uint8_t*>(a.dx) + offset(row, j) * kD;
+      uint8_t* dx = static_cast<uint8_t*>(a.dx) + offset(row, j) * kD + h0 * kD;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
 #pragma unroll
