@@ -30,6 +30,8 @@ struct RouteArgs {
 // A masked logit or bias: NaN, -inf or the lowest finite value.
 MOE_DEV bool absent(float v) { return !(v > -FLT_MAX); }
 
+MOE_DEV bool valid_expert(int e, int E) { return e >= 0 && e < E; }
+
 // Order-preserving integer keys, above 1 for every finite value that is not -FLT_MAX.  0 is
 // kept for experts out of the choice, 1 for masked experts of the kept groups.
 MOE_DEV uint32_t order_bits(float x) {
@@ -89,6 +91,30 @@ struct Token {
   uint32_t masked;   // bit i: left out of the choice (logit or bias)
   uint32_t lmasked;  // bit i: logit masked (scores 0)
 };
+
+template <int NG>
+MOE_DEV void load_token(const RouteArgs& a, long long row, Token<NG>& t) {
+  t.present = t.masked = t.lmasked = 0;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int e = (threadIdx.x & 31) * NG + i;
+    const bool in = e < a.E;
+    const float l = in ? __ldg(a.logits + row * a.E + e) : -INFINITY;
+    const float b = in && a.bias ? __ldg(a.bias + e) : 0.f;
+    const bool lm = absent(l);
+    t.present |= (uint32_t)in << i;
+    t.lmasked |= (uint32_t)lm << i;
+    t.masked |= (uint32_t)(lm || absent(b)) << i;
+    t.l[i] = fminf(l, FLT_MAX);
+    t.b[i] = fminf(b, FLT_MAX);
+  }
+}
+
+// log s up to the token's constant: renormalised weights are a softmax over it, so that no score
+// underflows.  log sigmoid(l) = min(l, 0) - log(1 + e^-|l|); the softmax's denominator cancels.
+MOE_DEV float log_score(float l, bool sigmoid) {
+  return sigmoid ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
+}
 
 // Selection slots: lane j % 32 holds selection j in slot j / 32.
 template <int NS>
@@ -180,7 +206,7 @@ MOE_DEV bool select(const RouteArgs& a, const Token<NG>& t, F* buf, Picked<NS>& 
       const unsigned out = __ballot_sync(kFull, mine && rank == a.top_groups);
       const F si = __shfl_sync(kFull, score, __ffs(in) - 1);
       const F so = __shfl_sync(kFull, score, __ffs(out) - 1);
-      if (so > (F)-INFINITY && si - so <= (F)group_margin((float)si)) return false;
+      if (so > (F)-INFINITY && !(si - so > (F)group_margin((float)si))) return false;
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
@@ -261,20 +287,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a) {
   const long long row = (long long)blockIdx.x * kWarps + warp;
   if (row >= a.T) return;  // warp-uniform
   Token<NG> t;
-  t.present = t.masked = t.lmasked = 0;
-#pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    const int e = lane * NG + i;
-    const bool in = e < a.E;
-    const float l = in ? __ldg(a.logits + row * a.E + e) : -INFINITY;
-    const float b = in && a.bias ? __ldg(a.bias + e) : 0.f;
-    const bool lm = absent(l);
-    t.present |= (uint32_t)in << i;
-    t.lmasked |= (uint32_t)lm << i;
-    t.masked |= (uint32_t)(lm || absent(b)) << i;
-    t.l[i] = fminf(l, FLT_MAX);
-    t.b[i] = fminf(b, FLT_MAX);
-  }
+  load_token<NG>(a, row, t);
   Picked<NS> p;
 #pragma unroll
   for (int q = 0; q < NS; ++q) p.ok[q] = false;
@@ -285,13 +298,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a) {
   // weights of the lane's selections
   float w[NS];
   if (a.renorm) {
-    // s_j / sum s_i as a softmax over log s_j: no score underflows.  log sigmoid(l) =
-    // min(l, 0) - log(1 + e^-|l|); the softmax's own denominator cancels.
     float v[NS], m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
       v[q] = -INFINITY;
-      if (p.ok[q]) v[q] = a.sigmoid ? fminf(p.l[q], 0.f) - log1pf(expf(-fabsf(p.l[q]))) : p.l[q];
+      if (p.ok[q]) v[q] = log_score(p.l[q], a.sigmoid);
       m = fmaxf(m, v[q]);
     }
     m = warp_maxf(m);
@@ -325,11 +336,329 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a) {
   }
 }
 
-// One warp per token: the row of d_logits is filled by the lanes together (zeros, or the dense
-// part of the softmax's gradient), then the k selected entries are added.
-template <int NG>
+// ---- four tokens per warp ---------------------------------------------------------------------
+// The form for k <= 8 (and groups, if any, of whole slots): eight lanes hold a token, lane q its
+// experts q, q + 8, ...  Each key becomes one 32-bit word, its place within the token's range of
+// keys in 23 bits above 255 - expert, so that words order by key and then by lower index, and a
+// compare-exchange is two instructions.  Words are sorted in registers (Batcher's odd-even merge
+// sort of K2 at a time), and two descending lists merge by max(a_i, b_{K2-1-i}), the K2 largest
+// of both, which a bitonic half-cleaner sorts; three such merges across lanes leave the token's
+// K2 largest in all eight.  A token whose order the 23 bits (or fp32 keys) cannot decide, or that
+// has fewer than k unmasked experts, goes through select() instead.
+template <int N>
+MOE_DEV void exchange(uint32_t (&v)[N], int i, int j) {  // the larger to i
+  const uint32_t a = max(v[i], v[j]), b = min(v[i], v[j]);
+  v[i] = a;
+  v[j] = b;
+}
+template <int N>
+MOE_DEV void sort_words(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) exchange(v, i + j, i + j + k);
+}
+template <int N>  // a := the N largest of a and b, both descending
+MOE_DEV void merge_words(uint32_t (&a)[N], const uint32_t (&b)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = max(a[i], b[N - 1 - i]);
+#pragma unroll
+  for (int d = N / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & d) == 0) exchange(a, i, i + d);
+}
+// Reductions over a token's eight lanes.
+template <class F, class Op>
+MOE_DEV F over8(F v, Op op) {
+#pragma unroll
+  for (int o = 1; o < 8; o *= 2) v = op(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+MOE_DEV float max8(float v) { return over8(v, [](float a, float b) { return fmaxf(a, b); }); }
+MOE_DEV float min8(float v) { return over8(v, [](float a, float b) { return fminf(a, b); }); }
+MOE_DEV float sum8(float v) { return over8(v, [](float a, float b) { return a + b; }); }
+
+// Two largest of a token's keys, joined.
+MOE_DEV void join_two(float& m1, float& m2, float o1, float o2) {
+  m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+  m1 = fmaxf(m1, o1);
+}
+
+// G: groups when a group is NS / G whole slots and E = 8 NS (a folded reduction then gives lane q
+// the score of group q), 1 without groups, 0 for other groups of whole slots.
+template <int NS, int K2, int G>
+__global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
+  constexpr int NG = NS / 4;  // experts a lane holds in select()
+  __shared__ double s_buf[4][32 * NG];
+  __shared__ float s_bias[8 * NS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = lane & 7, tok = lane >> 3;
+  const long long row0 = ((long long)blockIdx.x * (blockDim.x >> 5) + warp) * 4;
+  const bool live = row0 + tok < a.T;
+  const long long row = live ? row0 + tok : a.T - 1;  // dead lanes repeat the last token
+  const float* lg = a.logits + row * a.E;
+  const bool biased = a.bias != nullptr;
+  // masked and missing experts hold the lowest finite value, below every other key
+  float x[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) x[i] = 8 * i + q < a.E ? __ldg(lg + 8 * i + q) : -FLT_MAX;
+  if (biased) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+      s_bias[e] = fminf(fmaxf(__ldg(a.bias + e), -FLT_MAX), FLT_MAX);
+    __syncthreads();
+  }
+  if (row0 >= a.T) return;  // warp-uniform
+#pragma unroll
+  for (int i = 0; i < NS; ++i) x[i] = fminf(fmaxf(x[i], -FLT_MAX), FLT_MAX);
+  // softmax statistics where scores or weights need them
+  float top = 0.f, total = 1.f;
+  const bool scored = biased || (G != 1 && a.best2);
+  if (!a.sigmoid && (scored || !a.renorm)) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < NS; ++i) m = fmaxf(m, x[i]);
+    top = max8(m);
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) z += expf(x[i] - top);
+    total = sum8(z);
+  }
+  // Scores as keys.  ex2.approx and rcp.approx are within 2 ulp and 1 ulp, the exponent's
+  // rounding moves e^-l by |l| 2^-24: a sigmoid is within 4.3 2^-24 of its value.  A softmax score
+  // is within 2^-22 plus what its sum is off, less than 2^-19 of the score: see `margin`.
+  const float inv_total = 1.f / total;
+  auto score = [&](float l) {
+    if (!a.sigmoid) return __expf(l - top) * inv_total;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-l)));
+    return r;
+  };
+  if (biased) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float b = 8 * i + q < a.E ? s_bias[8 * i + q] : 0.f;
+      x[i] = x[i] > -FLT_MAX ? score(x[i]) + b : -FLT_MAX;
+    }
+  }
+  const float unit_margin = 0x1p-20f + (a.sigmoid ? 0.f : 0x1p-18f * inv_total);
+  bool unsure = false;
+  if constexpr (G != 1) {
+    float mine = -FLT_MAX;  // lane q: score of group q
+    const bool from_scores = !biased && a.best2;
+    int span = 0;
+    float v1[G ? G : 1], v2[G ? G : 1];
+    if constexpr (G > 1) {
+      constexpr int kSpan = NS / G;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        v1[g] = v2[g] = -FLT_MAX;
+#pragma unroll
+        for (int i = 0; i < kSpan; ++i) {
+          const float k = x[g * kSpan + i];
+          const float v = from_scores && k > -FLT_MAX ? score(k) : k;
+          v2[g] = fmaxf(v2[g], fminf(v1[g], v));
+          v1[g] = fmaxf(v1[g], v);
+        }
+      }
+      // halve the groups a lane keeps while joining it with the lane that keeps the others
+#pragma unroll
+      for (int n = G / 2, o = 4; o >= 1; o /= 2, n /= 2) {
+        const bool upper = q & o;
+        if (n >= 1) {
+#pragma unroll
+          for (int g = 0; g < G / 2; ++g)
+            if (g < n) {
+              const float k1 = upper ? v1[g + n] : v1[g], k2 = upper ? v2[g + n] : v2[g];
+              const float s1 = upper ? v1[g] : v1[g + n], s2 = upper ? v2[g] : v2[g + n];
+              v1[g] = k1;
+              v2[g] = k2;
+              join_two(v1[g], v2[g], __shfl_xor_sync(kFull, s1, o), __shfl_xor_sync(kFull, s2, o));
+            }
+        } else {
+          join_two(v1[0], v2[0], __shfl_xor_sync(kFull, v1[0], o), __shfl_xor_sync(kFull, v2[0], o));
+        }
+      }
+      // lane q holds group q / (8 / G)
+      const int from = (lane & 24) | (q * (8 / G) & 7);
+      mine = v1[0] + (a.best2 && v2[0] > -FLT_MAX ? v2[0] : 0.f);
+      mine = __shfl_sync(kFull, mine, from);
+    } else {
+      span = a.gsize >> 3;  // slots of a group
+      float m1 = -FLT_MAX, m2 = -FLT_MAX;
+      int g = 0, left = span;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (8 * i < a.E) {
+          const float v = from_scores && x[i] > -FLT_MAX ? score(x[i]) : x[i];
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+          if (--left == 0) {  // the group's two largest over the eight lanes
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2)
+              join_two(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
+            if (q == g) mine = m1 + (a.best2 && m2 > -FLT_MAX ? m2 : 0.f);
+            ++g;
+            left = span;
+            m1 = m2 = -FLT_MAX;
+          }
+        }
+      }
+    }
+    int rank = 0;
+#pragma unroll
+    for (int o = 1; o < 8; ++o) {
+      const int other = (q + o) & 7;
+      const float v = __shfl_sync(kFull, mine, (lane & 24) | other);
+      rank += other < a.groups && (v > mine || (v == mine && other < q)) ? 1 : 0;
+    }
+    const bool real = q < a.groups, kept = real && rank < a.top_groups;
+    if (scored) {
+      const float in = min8(kept ? mine : INFINITY), no = max8(real && !kept ? mine : -FLT_MAX);
+      unsure = no > -FLT_MAX && !(in - no > 2.f * unit_margin + 0x1p-21f * fabsf(in));
+    }
+    const uint32_t keep = __ballot_sync(kFull, kept) >> (lane & 24);
+    if constexpr (G > 1) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < NS / G; ++i) x[g * (NS / G) + i] = (keep >> g) & 1u ? x[g * (NS / G) + i] : -FLT_MAX;
+    } else {
+      int g = 0, left = span;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        x[i] = (keep >> g) & 1u ? x[i] : -FLT_MAX;
+        if (--left == 0) {
+          ++g;
+          left = span;
+        }
+      }
+    }
+  }
+  // words: the key's place below the largest one, 1 .. 2^23 - 1, above 255 - expert.  The eight
+  // lanes' largest keys are eight keys, so the k largest reach down to the least of these (lo):
+  // they have the places above 1024, and place 1 (masked, dropped, far below) is never chosen.
+  float hi = x[0];
+#pragma unroll
+  for (int i = 1; i < NS; ++i) hi = fmaxf(hi, x[i]);
+  const float lo = min8(hi);
+  hi = max8(hi);
+  unsure |= !(hi > -FLT_MAX);
+  const float range = fminf(fmaxf(hi - lo, 1e-30f), 64.f);
+  const float per = 8387582.f / range;
+  uint32_t word[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const float f = fmaxf(fmaf(x[i] - hi, per, 16777215.f), 8388609.f);
+    word[i] = (__float_as_uint(f) << 8) + (uint32_t)(255 - 8 * i - q);
+  }
+  uint32_t best[K2];
+#pragma unroll
+  for (int i = 0; i < K2; ++i) best[i] = i < NS ? word[i] : 0u;
+  sort_words(best);
+#pragma unroll
+  for (int c = K2; c < NS; c += K2) {
+    uint32_t next[K2];
+#pragma unroll
+    for (int i = 0; i < K2; ++i) next[i] = word[c + i];
+    sort_words(next);
+    merge_words(best, next);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o *= 2) {
+    uint32_t next[K2];
+#pragma unroll
+    for (int i = 0; i < K2; ++i) next[i] = __shfl_xor_sync(kFull, best[i], o);
+    merge_words(best, next);
+  }
+  // lane q takes selection q; the last one bounds what was left out
+  uint32_t mine = best[0], last = best[0];
+#pragma unroll
+  for (int i = 1; i < K2; ++i) {
+    mine = q == i ? best[i] : mine;
+    last = a.k - 1 == i ? best[i] : last;
+  }
+  const bool slot = q < a.k;
+  int e = slot ? 255 - (int)(mine & 255u) : 0;
+  unsure |= last < (2u << 8);  // an expert out of the choice
+  e = e < a.E ? e : 0;
+  float l = fminf(__ldg(lg + e), FLT_MAX);
+  float b = biased ? __ldg(a.bias + e) : 0.f;
+  {
+    // places nearer than the keys' error (none for logits) need equal logits and biases
+    const uint32_t near =
+        biased ? (uint32_t)fminf((unit_margin + 0x1p-22f * (fabsf(hi) + range)) * per, 8388607.f) + 1u : 0u;
+    const uint32_t below = __shfl_down_sync(kFull, mine, 1, 8);
+    const float l1 = __shfl_down_sync(kFull, l, 1, 8), b1 = __shfl_down_sync(kFull, b, 1, 8);
+    unsure |= q + 1 < a.k && (mine >> 8) - (below >> 8) <= near && !(l == l1 && b == b1);
+    const uint32_t reach = (last >> 8) > near ? ((last >> 8) - near) << 8 : 256u;
+    bool close = false;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) close |= word[i] - reach < last - reach;  // reach <= word < last
+    if (__any_sync(kFull, close)) {  // exact ties with the last one are in order
+      const float lk = __shfl_sync(kFull, l, (lane & 24) | (a.k - 1));
+      const float bk = __shfl_sync(kFull, b, (lane & 24) | (a.k - 1));
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (word[i] - reach < last - reach) {
+          const int o = 8 * i + q;
+          unsure |= !(fminf(__ldg(lg + o), FLT_MAX) == lk && (!biased || __ldg(a.bias + o) == bk));
+        }
+    }
+  }
+  bool ok = true;
+  unsigned again = __ballot_sync(kFull, unsure && live);
+  if (again) {
+    for (int t = 0; t < 4; ++t) {
+      if (!((again >> (8 * t)) & 0xFFu)) continue;  // warp-uniform
+      Token<NG> tk;
+      load_token<NG>(a, row0 + t, tk);
+      Picked<1> p;
+      p.ok[0] = false;
+      if (scored) select<double, NG, 1>(a, tk, s_buf[warp], p);
+      else select<float, NG, 1>(a, tk, reinterpret_cast<float*>(s_buf[warp]), p);
+      __syncwarp();
+      const int pe = __shfl_sync(kFull, p.e[0], q);
+      const float pl = __shfl_sync(kFull, p.l[0], q);
+      const bool po = __shfl_sync(kFull, (int)p.ok[0], q);
+      if (tok == t) {
+        e = pe;
+        l = pl;
+        ok = po;
+      }
+    }
+  }
+  ok = ok && slot;
+  float w;
+  if (a.renorm) {
+    const float v = !ok ? -INFINITY : log_score(l, a.sigmoid), m = max8(v);
+    const float z = ok ? expf(v - m) : 0.f, sum = sum8(z);
+    w = m > -INFINITY ? z * (a.scale / sum) : 0.f;
+  } else if (a.sigmoid) {
+    w = ok ? a.scale / (1.f + expf(-l)) : 0.f;
+  } else {
+    w = ok ? a.scale * (expf(l - top) / total) : 0.f;
+  }
+  if (slot && live) {
+    a.idx[row * a.k + q] = e;
+    a.w[row * a.k + q] = w;
+    if (a.counts) atomicAdd(a.counts + e, 1);
+  }
+}
+
+// One warp per token.  The row of d_logits is laid out in shared memory (zeros, or the dense part
+// of the softmax's gradient), the selected entries are added there, and the row leaves in vectors
+// of V floats (4 where E and the pointers allow it).  Bound by the rows of d_logits.
+template <int NV, int V>
 __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(
     RouteArgs a, const float* __restrict__ d_w, float* __restrict__ d_logits) {
+  struct alignas(4 * V) Vec { float f[V]; };
+  __shared__ Vec s_row[kWarps][32 * NV];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row = (long long)blockIdx.x * kWarps + warp;
   if (row >= a.T) return;  // warp-uniform
@@ -337,65 +666,96 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(
   const int32_t* idx = a.idx + row * a.k;
   const float* w = a.w + row * a.k;
   const float* dw = d_w + row * a.k;
-  float dot = 0.f;  // sum_j w_j dw_j; a weight of exactly 0 (masked) takes no part
-  for (int j = lane; j < a.k; j += 32) {
-    const float wj = w[j];
-    dot += wj != 0.f ? wj * dw[j] : 0.f;
-  }
-  dot = warp_sum(dot);
+  const int vecs = a.E / V;
   const bool dense = !a.sigmoid && !a.renorm;
-  float out[NG];
-#pragma unroll
-  for (int i = 0; i < NG; ++i) out[i] = 0.f;
+  float l[NV][V];
   if (dense) {
-    float l[NG], m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int e = lane + 32 * i;
-      const float v = e < a.E ? __ldg(lg + e) : -INFINITY;
-      l[i] = absent(v) ? -INFINITY : fminf(v, FLT_MAX);
-      m = fmaxf(m, l[i]);
+    for (int i = 0; i < NV; ++i) {
+      const int c = lane + 32 * i;
+      Vec v;
+#pragma unroll
+      for (int u = 0; u < V; ++u) v.f[u] = -INFINITY;
+      if (c < vecs) v = *reinterpret_cast<const Vec*>(lg + V * c);
+#pragma unroll
+      for (int u = 0; u < V; ++u) l[i][u] = absent(v.f[u]) ? -INFINITY : fminf(v.f[u], FLT_MAX);
     }
+  }
+  // the lane's slot; a weight of exactly 0 (masked) takes no part
+  const bool has = lane < a.k;
+  int e = has ? __ldg(idx + lane) : -1;
+  const float w0 = has ? __ldg(w + lane) : 0.f, dw0 = has && w0 != 0.f ? __ldg(dw + lane) : 0.f;
+  float dot = w0 * dw0;
+  for (int j = lane + 32; j < a.k; j += 32) {
+    const float wj = __ldg(w + j);
+    dot += wj != 0.f ? wj * __ldg(dw + j) : 0.f;
+  }
+  const float rest = a.sigmoid && valid_expert(e, a.E) ? 1.f + expf(__ldg(lg + e)) : 1.f;  // 1 / (1 - sigmoid(l))
+  dot = warp_sum(dot);
+  Vec* mine = s_row[warp];
+  float* flat = mine[0].f;
+  float scale = 0.f;
+  if (dense) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int u = 0; u < V; ++u) m = fmaxf(m, l[i][u]);
     m = warp_maxf(m);
-    if (m > -INFINITY) {
-      float z = 0.f;
+    float z = 0.f;
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        l[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.f;
-        z += l[i];
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        l[i][u] = l[i][u] > -INFINITY ? expf(l[i][u] - m) : 0.f;
+        z += l[i][u];
       }
-      z = warp_sum(z);
-      const float c = -dot / z;
+    z = warp_sum(z);
+    scale = z > 0.f ? -dot / z : 0.f;
+  }
 #pragma unroll
-      for (int i = 0; i < NG; ++i) out[i] = c * l[i];
-    }
+  for (int i = 0; i < NV; ++i) {
+    Vec v;
+#pragma unroll
+    for (int u = 0; u < V; ++u) v.f[u] = dense ? scale * l[i][u] : 0.f;
+    mine[lane + 32 * i] = v;
   }
   const float shared = a.renorm ? dot * a.inv_scale : 0.f;
-  for (int j0 = 0; j0 < a.k; j0 += 32) {
-    const int j = j0 + lane;
-    int e = -1;
-    float q = 0.f;
-    if (j < a.k) {
-      const float wj = w[j];
-      e = idx[j];
-      if (wj != 0.f && e >= 0 && e < a.E) {
-        q = wj * (dw[j] - shared);
-        if (a.sigmoid) q /= 1.f + expf(__ldg(lg + e));  // 1 - sigmoid(l)
+  float q = w0 != 0.f ? w0 * (dw0 - shared) / rest : 0.f;
+  __syncwarp();
+  for (int j0 = 0;;) {
+    // slots that name the same expert are added one after another, in order
+    const bool put = valid_expert(e, a.E);
+    const unsigned same = __match_any_sync(kFull, put ? e : -1 - lane);
+    if (!__any_sync(kFull, __popc(same) > 1)) {
+      if (put) flat[e] += q;
+    } else {
+      for (int i = 0; i < 32; ++i) {
+        if (lane == i && put) flat[e] += q;
+        __syncwarp();
       }
     }
-    const int n = min(32, a.k - j0);
-    for (int i0 = 0; i0 < n; ++i0) {
-      const int ee = __shfl_sync(kFull, e, i0);
-      const float qq = __shfl_sync(kFull, q, i0);
-#pragma unroll
-      for (int i = 0; i < NG; ++i)
-        if (ee == lane + 32 * i) out[i] += qq;
+    __syncwarp();
+    j0 += 32;
+    if (j0 >= a.k) break;
+    const int j = j0 + lane;
+    e = -1;
+    q = 0.f;
+    if (j < a.k) {
+      const float wj = __ldg(w + j);
+      e = __ldg(idx + j);
+      if (wj != 0.f && valid_expert(e, a.E)) {
+        q = wj * (__ldg(dw + j) - shared);
+        if (a.sigmoid) q /= 1.f + expf(__ldg(lg + e));
+      }
     }
   }
   float* o = d_logits + row * a.E;
 #pragma unroll
-  for (int i = 0; i < NG; ++i)
-    if (lane + 32 * i < a.E) o[lane + 32 * i] = out[i];
+  for (int i = 0; i < NV; ++i) {
+    const int c = lane + 32 * i;
+    if (c < vecs) *reinterpret_cast<Vec*>(o + V * c) = mine[c];
+  }
 }
 
 // One block per 32-token segment: slots copied, checked and counted per expert.
@@ -425,6 +785,8 @@ __global__ void __launch_bounds__(256) import_routing_kernel(
   for (int e = threadIdx.x; e < E; e += 256) hist[(size_t)seg * E + e] = s_hist[e];
 }
 
+template <int N> struct Slots { static constexpr int value = N; };
+
 RouteArgs route_args(const mxfp4_moe_routing& r) {
   RouteArgs a{};
   a.T = r.T; a.E = r.E; a.k = r.k;
@@ -441,7 +803,7 @@ RouteArgs route_args(const mxfp4_moe_routing& r) {
 }  // namespace
 
 cudaError_t launch_route(const mxfp4_moe_routing& r, const float* logits, const float* bias,
-                         int32_t* idx, float* w, int32_t* counts, int, cudaStream_t st) {
+                         int32_t* idx, float* w, int32_t* counts, int sms, cudaStream_t st) {
   if (counts) {
     const cudaError_t e = cudaMemsetAsync(counts, 0, 4 * (size_t)r.E, st);
     if (e != cudaSuccess) return e;
@@ -450,6 +812,22 @@ cudaError_t launch_route(const mxfp4_moe_routing& r, const float* logits, const 
   RouteArgs a = route_args(r);
   a.logits = logits; a.bias = bias; a.idx = idx; a.w = w; a.counts = counts;
   const int ng = (r.E + 31) / 32;
+  if (r.k <= 8 && (r.groups == 1 || (a.gsize % 8 == 0 && r.groups <= 8))) {
+    auto pick = [&](auto slots) {
+      constexpr int kNS = decltype(slots)::value;
+      const bool whole = r.E == 8 * kNS;
+      if (r.groups == 1) return r.k <= 4 ? route4_kernel<kNS, 4, 1> : route4_kernel<kNS, 8, 1>;
+      if constexpr (kNS >= 8)
+        if (whole && r.groups == 8) return r.k <= 4 ? route4_kernel<kNS, 4, 8> : route4_kernel<kNS, 8, 8>;
+      if (whole && r.groups == 4) return r.k <= 4 ? route4_kernel<kNS, 4, 4> : route4_kernel<kNS, 8, 4>;
+      return r.k <= 4 ? route4_kernel<kNS, 4, 0> : route4_kernel<kNS, 8, 0>;
+    };
+    auto kern = ng <= 1 ? pick(Slots<4>{}) : ng <= 2 ? pick(Slots<8>{}) : ng <= 4 ? pick(Slots<16>{}) : pick(Slots<32>{});
+    const long long warps = ((long long)r.T + 3) / 4;
+    const int per = warps >= 4 * sms ? 4 : 1;  // few tokens: a warp to an SM
+    kern<<<(unsigned)((warps + per - 1) / per), 32 * per, 0, st>>>(a);
+    return cudaGetLastError();
+  }
   const bool one = r.k <= 32;
   auto kern = ng <= 1   ? route_kernel<1, 1>
               : ng <= 2 ? (one ? route_kernel<2, 1> : route_kernel<2, 2>)
@@ -467,11 +845,14 @@ cudaError_t launch_route_backward(const mxfp4_moe_routing& r, const float* logit
   a.logits = logits;
   a.idx = const_cast<int32_t*>(idx);
   a.w = const_cast<float*>(w);
-  const int ng = (r.E + 31) / 32;
-  auto kern = ng <= 1   ? route_backward_kernel<1>
-              : ng <= 2 ? route_backward_kernel<2>
-              : ng <= 4 ? route_backward_kernel<4>
-                        : route_backward_kernel<8>;
+  const bool vec = r.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) |
+                                      reinterpret_cast<uintptr_t>(d_logits)) & 15u) == 0;
+  const int nv = ((vec ? r.E / 4 : r.E) + 31) / 32;
+  auto kern = vec       ? (nv <= 1 ? route_backward_kernel<1, 4> : route_backward_kernel<2, 4>)
+              : nv <= 1 ? route_backward_kernel<1, 1>
+              : nv <= 2 ? route_backward_kernel<2, 1>
+              : nv <= 4 ? route_backward_kernel<4, 1>
+                        : route_backward_kernel<8, 1>;
   kern<<<(unsigned)(((long long)r.T + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(a, d_w, d_logits);
   return cudaGetLastError();
 }
