@@ -72,6 +72,12 @@ MOE_DEV float warp_maxf(float v) {
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
   return v;
 }
+constexpr float kLog2e = 1.4426950408889634f;
+MOE_DEV float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 MOE_DEV float exp_of(float x) { return expf(x); }
 MOE_DEV double exp_of(double x) { return exp(x); }
 
@@ -391,8 +397,8 @@ MOE_DEV void join_two(float& m1, float& m2, float o1, float o2) {
 }
 
 // G: groups when a group is NS / G whole slots and E = 8 NS (a folded reduction then gives lane q
-// the score of group q), 1 without groups, 0 for other groups of whole slots.
-template <int NS, int K2, int G>
+// the score of group q), 1 without groups, 0 for other groups of whole slots.  WHOLE: E = 8 NS.
+template <int NS, int K2, int G, bool WHOLE>
 __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   constexpr int NG = NS / 4;  // experts a lane holds in select()
   __shared__ double s_buf[4][32 * NG];
@@ -404,18 +410,19 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   const long long row = live ? row0 + tok : a.T - 1;  // dead lanes repeat the last token
   const float* lg = a.logits + row * a.E;
   const bool biased = a.bias != nullptr;
-  // masked and missing experts hold the lowest finite value, below every other key
+  // masked and missing experts hold the lowest finite value, below every other key; a token with
+  // a logit of +inf is left to select()
   float x[NS];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) x[i] = 8 * i + q < a.E ? __ldg(lg + 8 * i + q) : -FLT_MAX;
+  for (int i = 0; i < NS; ++i) x[i] = WHOLE || 8 * i + q < a.E ? __ldg(lg + 8 * i + q) : -FLT_MAX;
   if (biased) {
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-      s_bias[e] = fminf(fmaxf(__ldg(a.bias + e), -FLT_MAX), FLT_MAX);
+    for (int e = threadIdx.x; e < 8 * NS; e += blockDim.x)
+      s_bias[e] = e < a.E ? fminf(fmaxf(__ldg(a.bias + e), -FLT_MAX), FLT_MAX) : 0.f;
     __syncthreads();
   }
   if (row0 >= a.T) return;  // warp-uniform
 #pragma unroll
-  for (int i = 0; i < NS; ++i) x[i] = fminf(fmaxf(x[i], -FLT_MAX), FLT_MAX);
+  for (int i = 0; i < NS; ++i) x[i] = fmaxf(x[i], -FLT_MAX);
   // softmax statistics where scores or weights need them
   float top = 0.f, total = 1.f;
   const bool scored = biased || (G != 1 && a.best2);
@@ -434,20 +441,19 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   // is within 2^-22 plus what its sum is off, less than 2^-19 of the score: see `margin`.
   const float inv_total = 1.f / total;
   auto score = [&](float l) {
-    if (!a.sigmoid) return __expf(l - top) * inv_total;
+    if (!a.sigmoid) return exp2_approx((l - top) * kLog2e) * inv_total;
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-l)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_approx(-kLog2e * l)));
     return r;
   };
   if (biased) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const float b = 8 * i + q < a.E ? s_bias[8 * i + q] : 0.f;
-      x[i] = x[i] > -FLT_MAX ? score(x[i]) + b : -FLT_MAX;
+      x[i] = x[i] > -FLT_MAX ? score(x[i]) + s_bias[8 * i + q] : -FLT_MAX;
     }
   }
   const float unit_margin = 0x1p-20f + (a.sigmoid ? 0.f : 0x1p-18f * inv_total);
-  bool unsure = false;
+  bool unsure = !(top < INFINITY);
   if constexpr (G != 1) {
     float mine = -FLT_MAX;  // lane q: score of group q
     const bool from_scores = !biased && a.best2;
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   for (int i = 1; i < NS; ++i) hi = fmaxf(hi, x[i]);
   const float lo = min8(hi);
   hi = max8(hi);
-  unsure |= !(hi > -FLT_MAX);
+  unsure |= !(hi > -FLT_MAX && hi < INFINITY);
   const float range = fminf(fmaxf(hi - lo, 1e-30f), 64.f);
   const float per = 8387582.f / range;
   uint32_t word[NS];
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   unsure |= last < (2u << 8);  // an expert out of the choice
   e = e < a.E ? e : 0;
   float l = fminf(__ldg(lg + e), FLT_MAX);
-  float b = biased ? __ldg(a.bias + e) : 0.f;
+  const float b = biased ? __ldg(a.bias + e) : 0.f;
   {
     // places nearer than the keys' error (none for logits) need equal logits and biases
     const uint32_t near =
@@ -648,6 +654,89 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
     a.idx[row * a.k + q] = e;
     a.w[row * a.k + q] = w;
     if (a.counts) atomicAdd(a.counts + e, 1);
+  }
+}
+
+// Four tokens per warp, for k <= 8: eight lanes hold a token's slots and the vectors q, q + 8, ...
+// of its row (V floats each: 4 where E and the pointers allow it).  The row is laid out in shared
+// memory (zeros, or the dense part of the softmax's gradient), the selected entries are added
+// there, and it leaves in vectors.  Bound by the rows of d_logits.
+template <int NV, int V>
+__global__ void __launch_bounds__(128) route4_backward_kernel(RouteArgs a, const float* __restrict__ d_w,
+                                                              float* __restrict__ d_logits) {
+  struct alignas(4 * V) Vec { float f[V]; };
+  __shared__ Vec s_row[4][4][8 * NV];
+  __shared__ uint8_t s_tag[4][4][8 * NV * V];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = lane & 7, tok = lane >> 3;
+  const long long row0 = ((long long)blockIdx.x * (blockDim.x >> 5) + warp) * 4;
+  if (row0 >= a.T) return;  // warp-uniform
+  const bool live = row0 + tok < a.T;
+  const long long row = live ? row0 + tok : a.T - 1;  // dead lanes repeat the last token
+  const float* lg = a.logits + row * a.E;
+  const int vecs = a.E / V;
+  const bool dense = !a.sigmoid && !a.renorm, has = q < a.k;
+  const int e = has ? __ldg(a.idx + row * a.k + q) : -1;
+  float w = has ? __ldg(a.w + row * a.k + q) : 0.f, dw = has ? __ldg(d_w + row * a.k + q) : 0.f;
+  const bool put = valid_expert(e, a.E);
+  const float le = a.sigmoid && put && w != 0.f ? __ldg(lg + e) : 0.f;
+  Vec row_v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int u = 0; u < V; ++u) row_v[i].f[u] = 0.f;
+  dw = w != 0.f ? dw : 0.f;  // a weight of exactly 0 (masked) takes no part
+  const float dot = sum8(w * dw);
+  if (dense) {
+    float m = -FLT_MAX, z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = 8 * i + q;
+      if (c < vecs) row_v[i] = *reinterpret_cast<const Vec*>(lg + V * c);
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        row_v[i].f[u] = c < vecs ? fminf(fmaxf(row_v[i].f[u], -FLT_MAX), FLT_MAX) : -FLT_MAX;
+        m = fmaxf(m, row_v[i].f[u]);
+      }
+    }
+    m = max8(m);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        row_v[i].f[u] = row_v[i].f[u] > -FLT_MAX ? expf(row_v[i].f[u] - m) : 0.f;
+        z += row_v[i].f[u];
+      }
+    z = sum8(z);
+    const float scale = z > 0.f ? -dot / z : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int u = 0; u < V; ++u) row_v[i].f[u] *= scale;
+  }
+  Vec* mine = s_row[warp][tok];
+  float* flat = mine[0].f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) mine[8 * i + q] = row_v[i];
+  // two slots that name one expert see it in its tag; they are added one after another
+  if (put) s_tag[warp][tok][e] = (uint8_t)q;
+  float d = w * (dw - (a.renorm ? dot * a.inv_scale : 0.f));
+  if (a.sigmoid) d /= 1.f + expf(le);  // times 1 - sigmoid(l)
+  __syncwarp();
+  if (!__any_sync(kFull, put && s_tag[warp][tok][e] != q)) {
+    if (put) flat[e] += d;
+  } else {
+    for (int j = 0; j < 8; ++j) {
+      if (put && q == j) flat[e] += d;
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+  float* o = d_logits + row * a.E;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * i + q;
+    if (c < vecs && live) *reinterpret_cast<Vec*>(o + V * c) = mine[c];
   }
 }
 
@@ -815,12 +904,15 @@ cudaError_t launch_route(const mxfp4_moe_routing& r, const float* logits, const 
   if (r.k <= 8 && (r.groups == 1 || (a.gsize % 8 == 0 && r.groups <= 8))) {
     auto pick = [&](auto slots) {
       constexpr int kNS = decltype(slots)::value;
-      const bool whole = r.E == 8 * kNS;
-      if (r.groups == 1) return r.k <= 4 ? route4_kernel<kNS, 4, 1> : route4_kernel<kNS, 8, 1>;
-      if constexpr (kNS >= 8)
-        if (whole && r.groups == 8) return r.k <= 4 ? route4_kernel<kNS, 4, 8> : route4_kernel<kNS, 8, 8>;
-      if (whole && r.groups == 4) return r.k <= 4 ? route4_kernel<kNS, 4, 4> : route4_kernel<kNS, 8, 4>;
-      return r.k <= 4 ? route4_kernel<kNS, 4, 0> : route4_kernel<kNS, 8, 0>;
+      const bool few = r.k <= 4;
+      if (r.E == 8 * kNS) {
+        if (r.groups == 1) return few ? route4_kernel<kNS, 4, 1, true> : route4_kernel<kNS, 8, 1, true>;
+        if constexpr (kNS >= 8)
+          if (r.groups == 8) return few ? route4_kernel<kNS, 4, 8, true> : route4_kernel<kNS, 8, 8, true>;
+        if (r.groups == 4) return few ? route4_kernel<kNS, 4, 4, true> : route4_kernel<kNS, 8, 4, true>;
+      }
+      if (r.groups == 1) return few ? route4_kernel<kNS, 4, 1, false> : route4_kernel<kNS, 8, 1, false>;
+      return few ? route4_kernel<kNS, 4, 0, false> : route4_kernel<kNS, 8, 0, false>;
     };
     auto kern = ng <= 1 ? pick(Slots<4>{}) : ng <= 2 ? pick(Slots<8>{}) : ng <= 4 ? pick(Slots<16>{}) : pick(Slots<32>{});
     const long long warps = ((long long)r.T + 3) / 4;
@@ -847,6 +939,20 @@ cudaError_t launch_route_backward(const mxfp4_moe_routing& r, const float* logit
   a.w = const_cast<float*>(w);
   const bool vec = r.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) |
                                       reinterpret_cast<uintptr_t>(d_logits)) & 15u) == 0;
+  if (r.k <= 8) {
+    const int n = (r.E + 31) / 32;
+    auto kern4 = vec ? (n <= 1   ? route4_backward_kernel<1, 4>
+                        : n <= 2 ? route4_backward_kernel<2, 4>
+                        : n <= 4 ? route4_backward_kernel<4, 4>
+                                 : route4_backward_kernel<8, 4>)
+                     : (n <= 1   ? route4_backward_kernel<4, 1>
+                        : n <= 2 ? route4_backward_kernel<8, 1>
+                        : n <= 4 ? route4_backward_kernel<16, 1>
+                                 : route4_backward_kernel<32, 1>);
+    const long long warps = ((long long)r.T + 3) / 4;
+    kern4<<<(unsigned)((warps + 3) / 4), 128, 0, st>>>(a, d_w, d_logits);
+    return cudaGetLastError();
+  }
   const int nv = ((vec ? r.E / 4 : r.E) + 31) / 32;
   auto kern = vec       ? (nv <= 1 ? route_backward_kernel<1, 4> : route_backward_kernel<2, 4>)
               : nv <= 1 ? route_backward_kernel<1, 1>
