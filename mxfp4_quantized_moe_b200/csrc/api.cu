@@ -1,5 +1,6 @@
 // C ABI of the MXFP4 MoE expert block: argument checks, workspace carving and the launch
 // sequence of the forward and input-gradient backward.  See include/mxfp4_moe.h.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -97,17 +98,25 @@ int check_weights(const mxfp4_moe_weights* w) {
   return MXFP4_MOE_OK;
 }
 
-// Current device must be sm_100 (B200).  Returns the SM count through `sms`.
+// Current device must be sm_100 (B200).  Returns the SM count through `sms`.  What a device is
+// never changes, so it is asked once and remembered (-1: another architecture).
 int check_device(int* sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MXFP4_MOE_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return MXFP4_MOE_ERR_CUDA;
-  if (major != 10 || minor != 0) return MXFP4_MOE_ERR_UNSUPPORTED_DEVICE;
-  if (sms && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MXFP4_MOE_ERR_CUDA;
+  int n = dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return MXFP4_MOE_ERR_CUDA;
+    if (major != 10 || minor != 0) n = -1;
+    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
+  }
+  if (n < 0) return MXFP4_MOE_ERR_UNSUPPORTED_DEVICE;
+  if (sms) *sms = n;
   return MXFP4_MOE_OK;
 }
 

@@ -1181,18 +1181,21 @@ bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Rows of a batch from which the forward takes its persistent form.
 constexpr int kManyRows = 600;
 
+template <class K>
+cudaError_t allow_shared(K kern, int bytes) {  // static shared memory included: 48 KB need no leave
+  if (bytes <= 32 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <int SRC, bool F32, bool RES, int NC, int RB, int NT, int BLOCKS>
 cudaError_t forward_persistent(const NormArgs& a, int W, int sms, cudaStream_t st) {
   auto kern = norm_forward_many_kernel<SRC, F32, RES, NC, RB, NT, BLOCKS>;
   const int groups = NT / (32 * W);
   const int smem = W * groups * RB * NC * kStage<SRC> * (RES ? 2 : 1);  // at most 128 KB
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * W * groups, smem);
+  const cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   const long long need = ((long long)a.T + RB * groups - 1) / (RB * groups);
-  const long long most = (long long)sms * (per_sm > 0 ? per_sm : 1);
+  const long long most = (long long)sms * BLOCKS;
   kern<<<(unsigned)(need < most ? need : most), 32 * W * groups, smem, st>>>(a, W);
   return cudaGetLastError();
 }
@@ -1263,7 +1266,7 @@ cudaError_t backward_staged(const NormGradArgs& a, int W, int* parts, cudaStream
   int smem = W * groups * R * NC * (kStage<SRC> + kStage<kGrad> * (HASG ? 2 : 1));
   const int sums = 4 * 256 * NC * W * groups;  // the groups' sums at the end
   if (smem < sums) smem = sums;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   const Share sh = share_rows(a.T, R * groups, BLOCKS);
   *parts = sh.blocks;

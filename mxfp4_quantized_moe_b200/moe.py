@@ -7,7 +7,6 @@ library's kernels.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import NamedTuple
@@ -224,19 +223,24 @@ def grad_chain(g: torch.Tensor, dx: torch.Tensor, d_logits: torch.Tensor, w_r: t
 # These run on the device of their tensors (all on one), whichever device is current, on that
 # device's current stream or on `stream`; what they allocate belongs to that stream.  Rows and
 # vectors are dense; every output that a caller may pass is also what the call returns.
-_HERE = contextlib.nullcontext()
 _EMPTY = 256  # stands for the null pointer of a tensor without elements; never dereferenced
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+_ROWS = (torch.bfloat16, torch.float32)
 
 
-def _at(device: torch.device, stream):
-    """Where a call on `device` allocates and launches."""
+def _elsewhere(device: torch.device, stream):
+    """The context in which a call on `device` allocates and launches; None: the present one."""
     if device.type != "cuda":
         raise ValueError("expected CUDA tensors")
     if stream is not None:
         if stream.device != device:
             raise ValueError("stream and tensors are on different devices")
         return torch.cuda.stream(stream)
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _current(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() costs 2 us more
 
 
 def _tensor(t: torch.Tensor, name: str, shape, dtypes, device) -> int:
@@ -252,19 +256,7 @@ def _tensor(t: torch.Tensor, name: str, shape, dtypes, device) -> int:
     return t.data_ptr() or _EMPTY
 
 
-def _output(t: torch.Tensor | None, name: str, shape, dtype, device):
-    """The caller's output, checked, or a new one: (tensor, data pointer)."""
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        return t, t.data_ptr() or _EMPTY
-    return t, _tensor(t, name, shape, (dtype,), device)
-
-
-_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
-_ROWS = (torch.bfloat16, torch.float32)
-
-
-@dataclass(frozen=True)
+@dataclass
 class Routing:
     """How tokens choose their experts (mxfp4_moe_routing in include/mxfp4_moe.h)."""
     k: int
@@ -282,10 +274,10 @@ class Routing:
                             self.group_best, int(self.renormalize), self.scale)
 
 
-def _logits(logits: torch.Tensor):
+def _logits_shape(logits: torch.Tensor):
     if logits.dim() != 2:
         raise ValueError("logits must be fp32 [T, E]")
-    return logits.shape, logits.device
+    return logits.shape
 
 
 def route(routing: Routing, logits: torch.Tensor, bias: torch.Tensor | None = None,
@@ -295,15 +287,27 @@ def route(routing: Routing, logits: torch.Tensor, bias: torch.Tensor | None = No
     balance bias fp32 [E] on the selection.  `counts` (int32 [E]) receives the slots of each
     expert.  Logits or biases of NaN, -inf or the lowest finite value mask an expert: it is
     selected last, with weight 0."""
-    (T, E), dev = _logits(logits)
-    with _at(dev, stream):
-        lp = _tensor(logits, "logits", (T, E), _F32, dev)
-        bp = None if bias is None else _tensor(bias, "bias", (E,), _F32, dev)
-        topk_idx, ip = _output(topk_idx, "topk_idx", (T, routing.k), torch.int32, dev)
-        topk_w, wp = _output(topk_w, "topk_w", (T, routing.k), torch.float32, dev)
-        cp = None if counts is None else _tensor(counts, "counts", (E,), _I32, dev)
-        dims = routing.dims(T, E)
-        check(lib.mxfp4_moe_route(dims, lp, bp, ip, wp, cp, _stream()), "mxfp4_moe_route")
+    T, E = _logits_shape(logits)
+    dev = logits.device
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return route(routing, logits, bias, topk_idx, topk_w, counts)
+    lp = _tensor(logits, "logits", (T, E), _F32, dev)
+    bp = None if bias is None else _tensor(bias, "bias", (E,), _F32, dev)
+    cp = None if counts is None else _tensor(counts, "counts", (E,), _I32, dev)
+    dims, slots = routing.dims(T, E), (T, routing.k)
+    if topk_idx is None:
+        topk_idx = torch.empty(slots, dtype=torch.int32, device=dev)
+        ip = topk_idx.data_ptr() or _EMPTY
+    else:
+        ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
+    if topk_w is None:
+        topk_w = logits.new_empty(slots)
+        wp = topk_w.data_ptr() or _EMPTY
+    else:
+        wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
+    check(lib.mxfp4_moe_route(dims, lp, bp, ip, wp, cp, _current(dev)), "mxfp4_moe_route")
     return topk_idx, topk_w
 
 
@@ -311,17 +315,24 @@ def route_backward(routing: Routing, logits: torch.Tensor, topk_idx: torch.Tenso
                    topk_w: torch.Tensor, d_topk_w: torch.Tensor,
                    d_logits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """d_logits fp32 [T, E] from d_topk_w fp32 [T, k], for what `route` returned on `logits`."""
-    (T, E), dev = _logits(logits)
+    T, E = _logits_shape(logits)
+    dev = logits.device
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return route_backward(routing, logits, topk_idx, topk_w, d_topk_w, d_logits)
     slots = (T, routing.k)
-    with _at(dev, stream):
-        lp = _tensor(logits, "logits", (T, E), _F32, dev)
-        ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
-        wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
-        dp = _tensor(d_topk_w, "d_topk_w", slots, _F32, dev)
-        d_logits, op = _output(d_logits, "d_logits", (T, E), torch.float32, dev)
-        dims = routing.dims(T, E)
-        check(lib.mxfp4_moe_route_backward(dims, lp, ip, wp, dp, op, _stream()),
-              "mxfp4_moe_route_backward")
+    lp = _tensor(logits, "logits", (T, E), _F32, dev)
+    ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
+    wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
+    dp = _tensor(d_topk_w, "d_topk_w", slots, _F32, dev)
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+        op = d_logits.data_ptr() or _EMPTY
+    else:
+        op = _tensor(d_logits, "d_logits", (T, E), _F32, dev)
+    check(lib.mxfp4_moe_route_backward(routing.dims(T, E), lp, ip, wp, dp, op, _current(dev)),
+          "mxfp4_moe_route_backward")
     return d_logits
 
 
@@ -332,17 +343,21 @@ def forward_routed(shape: MoeShape, w: dict, x: torch.Tensor, topk_idx: torch.Te
     [T, k]).  `backward_input(..., want_d_logits=False)` follows it; its d_topk_w goes on to
     `route_backward`."""
     dev = x.device
-    slots = (shape.T, shape.k)
-    with _at(dev, stream):
-        xp = _tensor(x, "x", (shape.T, shape.H), (torch.bfloat16,), dev)
-        ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
-        wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
-        if ws.device != dev:
-            raise ValueError(f"ws is on {ws.device}, expected {dev}")
-        y, yp = _output(y, "y", (shape.T, shape.H), torch.bfloat16, dev)
-        check(lib.mxfp4_moe_forward_routed(shape.dims(), _weights(w), xp, ip, wp, yp, _ptr(ws),
-                                           ws.numel() * ws.element_size(), _stream()),
-              "mxfp4_moe_forward_routed")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return forward_routed(shape, w, x, topk_idx, topk_w, ws, y)
+    rows, slots = (shape.T, shape.H), (shape.T, shape.k)
+    xp = _tensor(x, "x", rows, (torch.bfloat16,), dev)
+    ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
+    wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
+    if ws.device != dev or any(t.device != dev for t in w.values()):
+        raise ValueError(f"ws and the weights must be on {dev}")
+    if y is None:
+        y = torch.empty_like(x)
+    check(lib.mxfp4_moe_forward_routed(
+        shape.dims(), _weights(w), xp, ip, wp, _tensor(y, "y", rows, (torch.bfloat16,), dev),
+        _ptr(ws), ws.numel() * ws.element_size(), _current(dev)), "mxfp4_moe_forward_routed")
     return y
 
 
@@ -358,8 +373,8 @@ class Checkpoint:
     def empty(T: int, H: int, format: str = "e4m3", device="cuda") -> "Checkpoint":
         if H % 32:
             raise ValueError("a checkpoint needs H to be a multiple of 32")
-        return Checkpoint(torch.empty(T, H, dtype=torch.uint8, device=device),
-                          torch.empty(T, H // 32, dtype=torch.uint8, device=device), format)
+        return Checkpoint(torch.empty((T, H), dtype=torch.uint8, device=device),
+                          torch.empty((T, H // 32), dtype=torch.uint8, device=device), format)
 
     def _abi(self, T: int, H: int, device) -> _lib.Checkpoint:
         if self.format not in _lib.CHECKPOINTS:
@@ -373,7 +388,7 @@ def _rows_shape(x):
     t = x.codes if isinstance(x, Checkpoint) else x
     if t.dim() != 2:
         raise ValueError("rows must be [T, H]")
-    return t.shape[0], t.shape[1], t.device
+    return (*t.shape, t.device)
 
 
 def _format(dtype: torch.dtype) -> int:
@@ -386,13 +401,15 @@ def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | Non
                     stream=None) -> Checkpoint:
     """Rows [T, H] (bf16 or fp32, H a multiple of 32) stored in 8 bits."""
     T, H, dev = _rows_shape(x)
-    with _at(dev, stream):
-        xp = _tensor(x, "x", (T, H), _ROWS, dev)
-        if out is None:
-            out = Checkpoint.empty(T, H, format, dev)
-        to = out._abi(T, H, dev)
-        check(lib.mxfp4_moe_checkpoint_pack(T, H, _format(x.dtype), xp, to, _stream()),
-              "mxfp4_moe_checkpoint_pack")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return checkpoint_pack(x, format, out)
+    xp = _tensor(x, "x", (T, H), _ROWS, dev)
+    if out is None:
+        out = Checkpoint.empty(T, H, format, dev)
+    check(lib.mxfp4_moe_checkpoint_pack(T, H, _format(x.dtype), xp, out._abi(T, H, dev),
+                                        _current(dev)), "mxfp4_moe_checkpoint_pack")
     return out
 
 
@@ -400,12 +417,17 @@ def checkpoint_unpack(checkpoint: Checkpoint, dtype: torch.dtype = torch.bfloat1
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The rows [T, H] that a checkpoint stands for, as bf16 or fp32."""
     T, H, dev = _rows_shape(checkpoint)
-    with _at(dev, stream):
-        fmt = _format(dtype)
-        frm = checkpoint._abi(T, H, dev)
-        out, op = _output(out, "out", (T, H), dtype, dev)
-        check(lib.mxfp4_moe_checkpoint_unpack(T, H, fmt, frm, op, _stream()),
-              "mxfp4_moe_checkpoint_unpack")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return checkpoint_unpack(checkpoint, dtype, out)
+    fmt = _format(dtype)
+    frm = checkpoint._abi(T, H, dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=dev)
+    op = _tensor(out, "out", (T, H), (dtype,), dev)
+    check(lib.mxfp4_moe_checkpoint_unpack(T, H, fmt, frm, op, _current(dev)),
+          "mxfp4_moe_checkpoint_unpack")
     return out
 
 
@@ -451,27 +473,41 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
     if y is None and x_out is not None:
         raise ValueError("x_out without a residual")
     dims = _norm_dims(T, H, kind, eps, dtype, weight, bias)
-    with _at(dev, stream):
-        if stored:
-            xp, frm = None, x._abi(T, H, dev)
-        else:
-            xp, frm = _tensor(x, "x", (T, H), _ROWS, dev), None
-        yp = op = mp = to = None
-        wp = None if weight is None else _tensor(weight, "weight", (H,), _ROWS, dev)
-        bp = None if bias is None else _tensor(bias, "bias", (H,), _ROWS, dev)
-        if y is not None:
-            yp = _tensor(y, "y", (T, H), (dtype,), dev)
-            x_out, op = _output(x_out, "x_out", (T, H), dtype, dev)
-        if checkpoint is not None:
-            if not isinstance(checkpoint, Checkpoint):
-                checkpoint = Checkpoint.empty(T, H, checkpoint, dev)
-            to = checkpoint._abi(T, H, dev)
-        out, np_ = _output(out, "out", (T, H), dtype, dev)
-        if kind == "layer" or mean is not None:
-            mean, mp = _output(mean, "mean", (T,), torch.float32, dev)
-        rstd, rp = _output(rstd, "rstd", (T,), torch.float32, dev)
-        check(lib.mxfp4_moe_norm_forward(dims, xp, frm, yp, wp, bp, op, to, np_, mp, rp,
-                                         _stream()), "mxfp4_moe_norm_forward")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return norm_forward(x, weight, bias, kind=kind, eps=eps, y=y, checkpoint=checkpoint,
+                                dtype=dtype, out=out, x_out=x_out, mean=mean, rstd=rstd)
+    rows, own = (T, H), (dtype,)
+    xp = frm = yp = op = mp = to = None
+    if stored:
+        frm = x._abi(T, H, dev)
+    else:
+        xp = _tensor(x, "x", rows, own, dev)
+    wp = None if weight is None else _tensor(weight, "weight", (H,), _ROWS, dev)
+    bp = None if bias is None else _tensor(bias, "bias", (H,), _ROWS, dev)
+    if y is not None:
+        yp = _tensor(y, "y", rows, own, dev)
+        if x_out is None:
+            x_out = torch.empty_like(x)
+        op = _tensor(x_out, "x_out", rows, own, dev)
+    if checkpoint is not None:
+        if not isinstance(checkpoint, Checkpoint):
+            checkpoint = Checkpoint.empty(T, H, checkpoint, dev)
+        to = checkpoint._abi(T, H, dev)
+    if out is None:
+        out = torch.empty(rows, dtype=dtype, device=dev) if stored else torch.empty_like(x)
+    np_ = _tensor(out, "out", rows, own, dev)
+    if mean is not None:
+        mp = _tensor(mean, "mean", (T,), _F32, dev)
+    elif kind == "layer":
+        mean = torch.empty(T, dtype=torch.float32, device=dev)
+        mp = mean.data_ptr() or _EMPTY
+    if rstd is None:
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    rp = _tensor(rstd, "rstd", (T,), _F32, dev)
+    check(lib.mxfp4_moe_norm_forward(dims, xp, frm, yp, wp, bp, op, to, np_, mp, rp,
+                                     _current(dev)), "mxfp4_moe_norm_forward")
     return NormOut(out, x_out, mean, rstd, checkpoint)
 
 
@@ -491,45 +527,57 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     T, H, dev = _rows_shape(x)
     dtype = d_out.dtype
     dims = _norm_dims(T, H, kind, 0.0, dtype, weight, None)
-    with _at(dev, stream):
-        dp = _tensor(d_out, "d_out", (T, H), _ROWS, dev)
-        if isinstance(x, Checkpoint):
-            xp, frm = None, x._abi(T, H, dev)
-        else:
-            xp, frm = _tensor(x, "x", (T, H), (dtype,), dev), None
-        if kind == "layer" and mean is None:
-            raise ValueError("the layer norm's backward needs the mean")
-        mp = None if mean is None else _tensor(mean, "mean", (T,), _F32, dev)
-        rp = _tensor(rstd, "rstd", (T,), _F32, dev)
-        wp = None if weight is None else _tensor(weight, "weight", (H,), _ROWS, dev)
-        gp = None if g is None else _tensor(g, "g", (T, H), (dtype,), dev)
-        dx, op = _output(dx, "dx", (T, H), dtype, dev)
-        dwp = dbp = wsp = None
-        ws_bytes = 0
-        if params:
-            d_weight, dwp = _output(d_weight, "d_weight", (H,), torch.float32, dev)
-            if kind == "layer" or d_bias is not None:
-                d_bias, dbp = _output(d_bias, "d_bias", (H,), torch.float32, dev)
-            if ws is None:
-                n = ctypes.c_size_t()
-                check(lib.mxfp4_moe_norm_workspace_size(dims, n), "mxfp4_moe_norm_workspace_size")
-                ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-            elif ws.device != dev:
-                raise ValueError(f"ws is on {ws.device}, expected {dev}")
-            wsp, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-        elif d_weight is not None or d_bias is not None:
-            raise ValueError("params=False with an output for the parameters' gradient")
-        check(lib.mxfp4_moe_norm_backward(dims, dp, xp, frm, mp, rp, wp, gp, op, dwp, dbp, wsp,
-                                          ws_bytes, _stream()), "mxfp4_moe_norm_backward")
+    if kind == "layer" and mean is None:
+        raise ValueError("the layer norm's backward needs the mean")
+    if not params and (d_weight is not None or d_bias is not None):
+        raise ValueError("params=False with an output for the parameters' gradient")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return norm_backward(d_out, x, mean, rstd, weight, kind=kind, g=g, params=params,
+                                 dx=dx, d_weight=d_weight, d_bias=d_bias, ws=ws)
+    rows, own = (T, H), (dtype,)
+    xp = frm = dwp = dbp = wsp = None
+    dp = _tensor(d_out, "d_out", rows, _ROWS, dev)
+    if isinstance(x, Checkpoint):
+        frm = x._abi(T, H, dev)
+    else:
+        xp = _tensor(x, "x", rows, own, dev)
+    mp = None if mean is None else _tensor(mean, "mean", (T,), _F32, dev)
+    rp = _tensor(rstd, "rstd", (T,), _F32, dev)
+    wp = None if weight is None else _tensor(weight, "weight", (H,), _ROWS, dev)
+    gp = None if g is None else _tensor(g, "g", rows, own, dev)
+    if dx is None:
+        dx = torch.empty_like(d_out)
+    op = _tensor(dx, "dx", rows, own, dev)
+    ws_bytes = 0
+    if params:
+        if d_weight is None:
+            d_weight = torch.empty(H, dtype=torch.float32, device=dev)
+        dwp = _tensor(d_weight, "d_weight", (H,), _F32, dev)
+        if d_bias is None and kind == "layer":
+            d_bias = torch.empty_like(d_weight)
+        if d_bias is not None:
+            dbp = _tensor(d_bias, "d_bias", (H,), _F32, dev)
+        if ws is None:
+            ws = torch.empty(_norm_scratch(dims), dtype=torch.uint8, device=dev)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous, on {dev}")
+        wsp, ws_bytes = ws.data_ptr() or None, ws.numel() * ws.element_size()
+    check(lib.mxfp4_moe_norm_backward(dims, dp, xp, frm, mp, rp, wp, gp, op, dwp, dbp, wsp,
+                                      ws_bytes, _current(dev)), "mxfp4_moe_norm_backward")
     return dx, d_weight, d_bias
+
+
+def _norm_scratch(dims: _lib.Norm) -> int:
+    n = ctypes.c_size_t()
+    check(lib.mxfp4_moe_norm_workspace_size(dims, n), "mxfp4_moe_norm_workspace_size")
+    return n.value
 
 
 def norm_workspace_bytes(T: int, H: int) -> int:
     """Scratch bytes of norm_backward with the parameters' gradients."""
-    n = ctypes.c_size_t()
-    check(lib.mxfp4_moe_norm_workspace_size(_lib.Norm(T, H, 0, 0.0, 0, 0), n),
-          "mxfp4_moe_norm_workspace_size")
-    return n.value
+    return _norm_scratch(_lib.Norm(T, H, 0, 0.0, 0, 0))
 
 
 def selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:
