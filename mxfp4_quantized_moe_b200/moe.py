@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -232,11 +233,11 @@ def _elsewhere(device: torch.device, stream):
     """The context in which a call on `device` allocates and launches; None: the present one."""
     if device.type != "cuda":
         raise ValueError("expected CUDA tensors")
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream and tensors are on different devices")
-        return torch.cuda.stream(stream)
-    return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream is None:
+        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream and tensors are on different devices")
+    return torch.cuda.stream(stream)
 
 
 def _current(device: torch.device) -> int:
@@ -268,10 +269,16 @@ class Routing:
     scale: float = 1.0
 
     def dims(self, T: int, E: int) -> _lib.Routing:
-        if self.scores not in _lib.SCORES:
-            raise ValueError(f"scores must be one of {sorted(_lib.SCORES)}")
-        return _lib.Routing(T, E, self.k, _lib.SCORES[self.scores], self.groups, self.top_groups,
-                            self.group_best, int(self.renormalize), self.scale)
+        return _routing_dims(T, E, self.k, self.scores, self.groups, self.top_groups,
+                             self.group_best, self.renormalize, self.scale)
+
+
+@lru_cache(maxsize=1024)  # the library only reads them
+def _routing_dims(T, E, k, scores, groups, top_groups, group_best, renormalize, scale):
+    if scores not in _lib.SCORES:
+        raise ValueError(f"scores must be one of {sorted(_lib.SCORES)}")
+    return _lib.Routing(T, E, k, _lib.SCORES[scores], groups, top_groups, group_best,
+                        int(renormalize), scale)
 
 
 def _logits_shape(logits: torch.Tensor):
@@ -425,7 +432,9 @@ def checkpoint_unpack(checkpoint: Checkpoint, dtype: torch.dtype = torch.bfloat1
     frm = checkpoint._abi(T, H, dev)
     if out is None:
         out = torch.empty((T, H), dtype=dtype, device=dev)
-    op = _tensor(out, "out", (T, H), (dtype,), dev)
+        op = out.data_ptr() or _EMPTY
+    else:
+        op = _tensor(out, "out", (T, H), (dtype,), dev)
     check(lib.mxfp4_moe_checkpoint_unpack(T, H, fmt, frm, op, _current(dev)),
           "mxfp4_moe_checkpoint_unpack")
     return out
@@ -439,14 +448,20 @@ class NormOut(NamedTuple):
     checkpoint: Checkpoint | None       # where one was asked for
 
 
-def _norm_dims(T, H, kind, eps, rows, weight, bias) -> _lib.Norm:
+@lru_cache(maxsize=1024)  # the library only reads them
+def _norm_dims(T, H, kind, eps, rows: torch.dtype, params: torch.dtype) -> _lib.Norm:
     if kind not in _lib.NORMS:
         raise ValueError(f"kind must be one of {sorted(_lib.NORMS)}")
-    p = weight if weight is not None else bias
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have the same type")
-    return _lib.Norm(T, H, _lib.NORMS[kind], eps, _format(rows),
-                     _lib.ROWS_BF16 if p is None else _format(p.dtype))
+    return _lib.Norm(T, H, _lib.NORMS[kind], eps, _format(rows), _format(params))
+
+
+@lru_cache(maxsize=1024)
+def norm_workspace_bytes(T: int, H: int) -> int:
+    """Scratch bytes of norm_backward with the parameters' gradients."""
+    n = ctypes.c_size_t()
+    check(lib.mxfp4_moe_norm_workspace_size(_lib.Norm(T, H, 0, 0.0, 0, 0), n),
+          "mxfp4_moe_norm_workspace_size")
+    return n.value
 
 
 def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = None,
@@ -472,7 +487,14 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
         dtype = x.dtype
     if y is None and x_out is not None:
         raise ValueError("x_out without a residual")
-    dims = _norm_dims(T, H, kind, eps, dtype, weight, bias)
+    params = dtype
+    if weight is not None:
+        params = weight.dtype
+        if bias is not None and bias.dtype != params:
+            raise TypeError("weight and bias must have the same type")
+    elif bias is not None:
+        params = bias.dtype
+    dims = _norm_dims(T, H, kind, eps, dtype, params)
     where = _elsewhere(dev, stream)
     if where is not None:
         with where:
@@ -490,22 +512,28 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
         yp = _tensor(y, "y", rows, own, dev)
         if x_out is None:
             x_out = torch.empty_like(x)
-        op = _tensor(x_out, "x_out", rows, own, dev)
+            op = x_out.data_ptr() or _EMPTY
+        else:
+            op = _tensor(x_out, "x_out", rows, own, dev)
     if checkpoint is not None:
         if not isinstance(checkpoint, Checkpoint):
             checkpoint = Checkpoint.empty(T, H, checkpoint, dev)
         to = checkpoint._abi(T, H, dev)
     if out is None:
         out = torch.empty(rows, dtype=dtype, device=dev) if stored else torch.empty_like(x)
-    np_ = _tensor(out, "out", rows, own, dev)
+        np_ = out.data_ptr() or _EMPTY
+    else:
+        np_ = _tensor(out, "out", rows, own, dev)
+    if rstd is None:
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        rp = rstd.data_ptr() or _EMPTY
+    else:
+        rp = _tensor(rstd, "rstd", (T,), _F32, dev)
     if mean is not None:
         mp = _tensor(mean, "mean", (T,), _F32, dev)
     elif kind == "layer":
-        mean = torch.empty(T, dtype=torch.float32, device=dev)
+        mean = torch.empty_like(rstd)
         mp = mean.data_ptr() or _EMPTY
-    if rstd is None:
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    rp = _tensor(rstd, "rstd", (T,), _F32, dev)
     check(lib.mxfp4_moe_norm_forward(dims, xp, frm, yp, wp, bp, op, to, np_, mp, rp,
                                      _current(dev)), "mxfp4_moe_norm_forward")
     return NormOut(out, x_out, mean, rstd, checkpoint)
@@ -526,7 +554,7 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     allocated); two captured graphs that may run at once need one each."""
     T, H, dev = _rows_shape(x)
     dtype = d_out.dtype
-    dims = _norm_dims(T, H, kind, 0.0, dtype, weight, None)
+    dims = _norm_dims(T, H, kind, 0.0, dtype, dtype if weight is None else weight.dtype)
     if kind == "layer" and mean is None:
         raise ValueError("the layer norm's backward needs the mean")
     if not params and (d_weight is not None or d_bias is not None):
@@ -549,35 +577,32 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     gp = None if g is None else _tensor(g, "g", rows, own, dev)
     if dx is None:
         dx = torch.empty_like(d_out)
-    op = _tensor(dx, "dx", rows, own, dev)
+        op = dx.data_ptr() or _EMPTY
+    else:
+        op = _tensor(dx, "dx", rows, own, dev)
     ws_bytes = 0
     if params:
         if d_weight is None:
             d_weight = torch.empty(H, dtype=torch.float32, device=dev)
-        dwp = _tensor(d_weight, "d_weight", (H,), _F32, dev)
-        if d_bias is None and kind == "layer":
-            d_bias = torch.empty_like(d_weight)
+            dwp = d_weight.data_ptr()
+        else:
+            dwp = _tensor(d_weight, "d_weight", (H,), _F32, dev)
         if d_bias is not None:
             dbp = _tensor(d_bias, "d_bias", (H,), _F32, dev)
+        elif kind == "layer":
+            d_bias = torch.empty_like(d_weight)
+            dbp = d_bias.data_ptr()
         if ws is None:
-            ws = torch.empty(_norm_scratch(dims), dtype=torch.uint8, device=dev)
+            ws_bytes = norm_workspace_bytes(T, H)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         elif ws.device != dev or not ws.is_contiguous():
             raise ValueError(f"ws must be contiguous, on {dev}")
-        wsp, ws_bytes = ws.data_ptr() or None, ws.numel() * ws.element_size()
+        else:
+            ws_bytes = ws.numel() * ws.element_size()
+        wsp = ws.data_ptr() or None
     check(lib.mxfp4_moe_norm_backward(dims, dp, xp, frm, mp, rp, wp, gp, op, dwp, dbp, wsp,
                                       ws_bytes, _current(dev)), "mxfp4_moe_norm_backward")
     return dx, d_weight, d_bias
-
-
-def _norm_scratch(dims: _lib.Norm) -> int:
-    n = ctypes.c_size_t()
-    check(lib.mxfp4_moe_norm_workspace_size(dims, n), "mxfp4_moe_norm_workspace_size")
-    return n.value
-
-
-def norm_workspace_bytes(T: int, H: int) -> int:
-    """Scratch bytes of norm_backward with the parameters' gradients."""
-    return _norm_scratch(_lib.Norm(T, H, 0, 0.0, 0, 0))
 
 
 def selftest_wait_timeout(ws: torch.Tensor, stream=None) -> None:
