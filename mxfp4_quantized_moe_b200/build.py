@@ -17,6 +17,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -47,25 +49,37 @@ def build(force: bool = False, ptxas_verbose: bool = False, debug: bool = False)
     lib = LIB_DEBUG if debug else LIB
     if not force and not needs_build(lib):
         return lib
-    cmd = [nvcc(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a",
-           "-lineinfo", "-Xcompiler", "-fPIC", "-shared", "-Xcompiler", "-fvisibility=hidden",
-           "-I", os.path.join(ROOT, "include"), "-o", lib + ".tmp"]
+    flags = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a",
+             "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+             "-I", os.path.join(ROOT, "include")]
     if debug:
-        cmd += ["-DMXFP4_MOE_DEBUG=1"]
+        flags += ["-DMXFP4_MOE_DEBUG=1"]
     if ptxas_verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += [os.path.join(HERE, s) for s in SOURCES]
-    r = subprocess.run(cmd, cwd=HERE, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+        flags += ["-Xptxas", "-v"]
+
+    def run(cmd):
+        r = subprocess.run([nvcc(), *cmd], cwd=HERE, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+        return r.stdout + r.stderr
+
+    # one compiler per source, then the link (no device code crosses a file)
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+            said = list(pool.map(lambda so: run([*flags, "-c", "-o", so[1],
+                                                 os.path.join(HERE, so[0])]), zip(SOURCES, objects)))
+        run(["-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", lib + ".tmp", *objects])
     if ptxas_verbose:
-        sys.stderr.write(r.stdout + r.stderr)
+        sys.stderr.write("".join(said))
     os.replace(lib + ".tmp", lib)
     return lib
 
 
 def build_all(force: bool = False, ptxas_verbose: bool = False) -> list[str]:
-    return [build(force, ptxas_verbose), build(force, False, debug=True)]
+    with ThreadPoolExecutor(max_workers=2) as pool:
+        both = [pool.submit(build, force, ptxas_verbose), pool.submit(build, force, False, True)]
+        return [b.result() for b in both]
 
 
 if __name__ == "__main__":

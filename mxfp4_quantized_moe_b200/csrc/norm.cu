@@ -193,20 +193,28 @@ MOE_DEV void decode8(uint2 q, uint32_t byte, float (&v)[8]) {
   const float s = scale_value(byte);
   const uint32_t w[2] = {q.x, q.y};
   if constexpr (FMT == kE4m3) {
+    const uint64_t s2 = f2(s, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t h2;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
       const __half2 hh = *reinterpret_cast<const __half2*>(&h2);
-      v[2 * i] = __low2float(hh) * s;
-      v[2 * i + 1] = __high2float(hh) * s;
+      const uint64_t p = f2mul(f2(__low2float(hh), __high2float(hh)), s2);
+      v[2 * i] = f2lo(p);
+      v[2 * i + 1] = f2hi(p);
     }
   } else {
+    // the byte with its sign bit flipped is code + 128, set into the fraction of 2^23
+    const float t = s * 0.015625f;
+    const uint64_t t2 = f2(t, t), z2 = f2(-8388736.f, -8388736.f);
+    const uint32_t x[2] = {w[0] ^ 0x80808080u, w[1] ^ 0x80808080u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // the byte with its sign bit flipped is code + 128, set into the fraction of 2^23
-      const uint32_t u = prmt(w[i >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440u | (uint32_t)(i & 3));
-      v[i] = (__uint_as_float(u) - 8388736.f) * 0.015625f * s;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = prmt(x[i >> 1], 0x4B000000u, 0x7440u | (uint32_t)(2 * i & 3));
+      const uint32_t hi = prmt(x[i >> 1], 0x4B000000u, 0x7440u | (uint32_t)(2 * i + 1 & 3));
+      const uint64_t p = f2mul(f2add(f2(__uint_as_float(lo), __uint_as_float(hi)), z2), t2);
+      v[2 * i] = f2lo(p);
+      v[2 * i + 1] = f2hi(p);
     }
   }
 }
@@ -1148,32 +1156,54 @@ __global__ void __launch_bounds__(32 * kReduceWarps) norm_reduce_kernel(
 }
 
 // ---- the checkpoint alone -------------------------------------------------------------------
+// Bound by the bytes; a thread takes kEach vectors, a block apart, so that their loads are in
+// flight together.
+constexpr int kEach = 4;
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256) checkpoint_pack_kernel(const void* x, long long chunks,
                                                               mxfp4_moe_checkpoint to) {
-  const long long c = (long long)blockIdx.x * 256 + threadIdx.x;
-  const bool in = c < chunks;  // whole blocks of four lanes
-  Row<F32, 8> r;
-  clear(r);
-  if (in) fetch<F32 ? kF32 : kBf16, 8>(r, x, (size_t)c * 8);
-  float v[8];
-  values<F32 ? kF32 : kBf16, 8>(r, v);
-  uint32_t byte;
-  const uint2 q = encode8<FMT>(v, byte);
-  if (in) {
-    reinterpret_cast<uint2*>(to.codes)[c] = q;
-    if ((c & 3) == 0) to.scales[c >> 2] = (uint8_t)byte;
+  const long long c0 = (long long)blockIdx.x * (256 * kEach) + threadIdx.x;
+  Row<F32, 8> r[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    clear(r[i]);
+    if (c0 + 256 * i < chunks) fetch<F32 ? kF32 : kBf16, 8>(r[i], x, (size_t)(c0 + 256 * i) * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const long long c = c0 + 256 * i;  // whole blocks of four lanes
+    float v[8];
+    values<F32 ? kF32 : kBf16, 8>(r[i], v);
+    uint32_t byte;
+    const uint2 q = encode8<FMT>(v, byte);
+    if (c < chunks) {
+      reinterpret_cast<uint2*>(to.codes)[c] = q;
+      if ((c & 3) == 0) to.scales[c >> 2] = (uint8_t)byte;
+    }
   }
 }
 
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256) checkpoint_unpack_kernel(mxfp4_moe_checkpoint from,
                                                                 long long chunks, void* x) {
-  const long long c = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (c >= chunks) return;
-  float v[8];
-  decode8<FMT>(__ldg(reinterpret_cast<const uint2*>(from.codes) + c), __ldg(from.scales + (c >> 2)), v);
-  store_rows<F32, 8>(x, (size_t)c * 8, v);
+  const long long c0 = (long long)blockIdx.x * (256 * kEach) + threadIdx.x;
+  uint2 q[kEach];
+  uint32_t byte[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    q[i] = make_uint2(0u, 0u);
+    byte[i] = 127u;
+    if (c0 + 256 * i < chunks) {
+      q[i] = __ldg(reinterpret_cast<const uint2*>(from.codes) + c0 + 256 * i);
+      byte[i] = __ldg(from.scales + ((c0 + 256 * i) >> 2));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    float v[8];
+    decode8<FMT>(q[i], byte[i], v);
+    if (c0 + 256 * i < chunks) store_rows<F32, 8>(x, (size_t)(c0 + 256 * i) * 8, v);
+  }
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1352,7 +1382,7 @@ cudaError_t launch_checkpoint_pack(int T, int H, bool rows_f32, const void* x,
                                    const mxfp4_moe_checkpoint& to, cudaStream_t st) {
   const long long chunks = (long long)T * H / 8;
   if (chunks == 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)((chunks + 255) / 256);
+  const unsigned blocks = (unsigned)((chunks + 256 * kEach - 1) / (256 * kEach));
   auto kern = to.format == MXFP4_MOE_CHECKPOINT_E4M3
                   ? (rows_f32 ? checkpoint_pack_kernel<kE4m3, true> : checkpoint_pack_kernel<kE4m3, false>)
                   : (rows_f32 ? checkpoint_pack_kernel<kInt8, true> : checkpoint_pack_kernel<kInt8, false>);
@@ -1364,7 +1394,7 @@ cudaError_t launch_checkpoint_unpack(int T, int H, bool rows_f32,
                                      const mxfp4_moe_checkpoint& from, void* x, cudaStream_t st) {
   const long long chunks = (long long)T * H / 8;
   if (chunks == 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)((chunks + 255) / 256);
+  const unsigned blocks = (unsigned)((chunks + 256 * kEach - 1) / (256 * kEach));
   auto kern = from.format == MXFP4_MOE_CHECKPOINT_E4M3
                   ? (rows_f32 ? checkpoint_unpack_kernel<kE4m3, true> : checkpoint_unpack_kernel<kE4m3, false>)
                   : (rows_f32 ? checkpoint_unpack_kernel<kInt8, true> : checkpoint_unpack_kernel<kInt8, false>);
