@@ -10,6 +10,16 @@ and derivative factors) in the layer's workspace, so a layer's backward must fol
 forward before that layer runs forward again: one MoeLayer per block in the graph, or
 recompute the forward before the backward (see stack.py).
 
+Around the block, in the same graph:
+
+    n = norm(x, weight, bias)                     # or (n, x_out) = norm(..., residual=y)
+    idx, w = route(logits, routing, bias)         # moe.Routing: scores, groups, balance bias
+    y = moe_block_routed(n, idx, w, layer)        # the block on that routing
+
+norm(..., checkpoint="e4m3" | "int8") keeps the rows for the backward in 8 bits.  The backwards of
+these cannot be captured into a CUDA graph (an eager graph over the same leaves would end the
+process); capture moe.norm_backward, moe.route_backward and moe.backward_input instead.
+
 Source: "Add MXFP4 training support via a dequantize-on-the-fly fallback" (sections "What this
 does" and "Relation to the backward triton kernels": gradients reach the inputs through the
 expert math; the frozen quantized base gets no weight gradient).
@@ -18,6 +28,7 @@ expert math; the frozen quantized base gets no weight gradient).
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import moe
 
@@ -60,3 +71,113 @@ class _MoeBlock(torch.autograd.Function):
 def moe_block(x: torch.Tensor, logits: torch.Tensor, layer: MoeLayer) -> torch.Tensor:
     """y = MoE(x, logits) with gradients to x and logits (bf16 x, fp32 logits, bf16 y)."""
     return _MoeBlock.apply(x, logits, layer)
+
+
+def _refuse_capture(what: str, instead: str) -> None:
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"{what}: the autograd backward cannot be captured into a CUDA graph; "
+                           f"capture {instead}")
+
+
+class _MoeBlockRouted(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, topk_idx, topk_w, layer: MoeLayer):
+        y = moe.forward_routed(layer.shape, layer.w, x.contiguous(), topk_idx.contiguous(),
+                               topk_w.contiguous(), layer.ws)
+        layer.forwards += 1
+        layer.consumed = False
+        ctx.layer = layer
+        ctx.forward_id = layer.forwards
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        layer = ctx.layer
+        _refuse_capture("moe_block_routed", "moe.backward_input")
+        if layer.forwards != ctx.forward_id or layer.consumed:
+            raise RuntimeError("MoeLayer: the workspace no longer holds this forward's state "
+                               "(another forward or backward of the layer ran in between)")
+        dx, d_topk_w, _ = moe.backward_input(layer.shape, layer.w, layer.wt,
+                                             dy.to(torch.bfloat16).contiguous(), layer.ws,
+                                             want_d_logits=False)
+        layer.consumed = True
+        return dx, None, d_topk_w, None
+
+
+def moe_block_routed(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                     layer: MoeLayer) -> torch.Tensor:
+    """The block on a given routing (topk_idx int32 [T, k], topk_w fp32 [T, k]), with gradients to
+    x and topk_w."""
+    return _MoeBlockRouted.apply(x, topk_idx, topk_w, layer)
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, routing, bias):
+        logits = logits.contiguous()
+        idx, w = moe.route(routing, logits, bias)
+        ctx.mark_non_differentiable(idx)
+        ctx.save_for_backward(logits, idx, w)
+        ctx.routing = routing
+        return idx, w
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, d_w):
+        _refuse_capture("route", "moe.route_backward")
+        logits, idx, w = ctx.saved_tensors
+        return moe.route_backward(ctx.routing, logits, idx, w, d_w.contiguous()), None, None
+
+
+def route(logits: torch.Tensor, routing: moe.Routing, bias: torch.Tensor | None = None):
+    """moe.route with the weights' gradient to the logits: (topk_idx, topk_w) of fp32 logits
+    [T, E].  The selection and the bias carry no gradient."""
+    return _Route.apply(logits, routing, None if bias is None else bias.detach())
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, kind, eps, checkpoint):
+        rows = x.contiguous().view(-1, x.shape[-1])
+        y = None if residual is None else residual.contiguous().view(rows.shape)
+        w = None if weight is None else weight.contiguous()
+        f = moe.norm_forward(rows, w, None if bias is None else bias.contiguous(), kind=kind,
+                             eps=eps, y=y, checkpoint=checkpoint)
+        kept = rows if y is None else f.x_out
+        if checkpoint:
+            kept, ctx.scales, ctx.format = f.checkpoint.codes, f.checkpoint.scales, checkpoint
+        ctx.save_for_backward(kept, f.mean, f.rstd, w)
+        ctx.kind, ctx.checkpoint, ctx.shape = kind, checkpoint, x.shape
+        ctx.bias_type = None if bias is None else bias.dtype
+        out = f.out.view(x.shape)
+        return out if residual is None else (out, f.x_out.view(x.shape))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out, d_x_out=None):
+        _refuse_capture("norm", "moe.norm_backward")
+        kept, mean, rstd, w = ctx.saved_tensors
+        rows = moe.Checkpoint(kept, ctx.scales, ctx.format) if ctx.checkpoint else kept
+        shape = kept.shape
+        g = None if d_x_out is None else d_x_out.contiguous().view(shape)
+        params = (w is not None and ctx.needs_input_grad[1]) or ctx.needs_input_grad[2]
+        dx, d_weight, d_bias = moe.norm_backward(
+            d_out.contiguous().view(shape), rows, mean, rstd, w, kind=ctx.kind, g=g, params=params,
+            d_bias=(torch.empty(shape[1], dtype=torch.float32, device=kept.device)
+                    if params and ctx.kind == "rms" and ctx.needs_input_grad[2] else None))
+        dx = dx.view(ctx.shape)
+        return (dx if ctx.needs_input_grad[0] else None,
+                d_weight.to(w.dtype) if params and ctx.needs_input_grad[1] else None,
+                d_bias.to(ctx.bias_type) if params and ctx.needs_input_grad[2] else None,
+                dx if ctx.needs_input_grad[3] else None, None, None, None)
+
+
+def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+         residual: torch.Tensor | None = None, kind: str = "layer", eps: float = 1e-5,
+         checkpoint: str | None = None):
+    """Layer or rms norm over the last dimension of x (bf16 or fp32), with gradients to x, weight,
+    bias and residual.  With a residual: (norm(x + residual), x + residual).  checkpoint ("e4m3" or
+    "int8", the last dimension a multiple of 32): the backward reads the rows from 8 bits, with
+    the statistics of the exact rows."""
+    return _Norm.apply(x, weight, bias, residual, kind, eps, checkpoint)

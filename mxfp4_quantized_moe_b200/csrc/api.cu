@@ -516,7 +516,7 @@ int mxfp4_moe_residual_router(int32_t T, int32_t H, int32_t E, const uint16_t* x
 int mxfp4_moe_grad_chain(int32_t T, int32_t H, int32_t E, const uint16_t* g, const uint16_t* dx,
                          const float* d_logits, const uint16_t* w_r, uint16_t* g_out,
                          void* stream) {
-  if (T < 0 || H < 32 || H % 32 || E < 1 || E > 256 || !g || !dx || !d_logits || !w_r || !g_out ||
+  if (T < 0 || H < 32 || H % 32 || E < 1 || E > 256 || !g || !d_logits || !w_r || !g_out ||
       !aligned16(g) || !aligned16(dx) || !aligned16(w_r) || !aligned16(g_out))
     return MXFP4_MOE_ERR_INVALID_ARG;
   const int rc = check_device(nullptr);

@@ -19,7 +19,7 @@ cudaError_t launch_interleave_gate_up(const uint8_t* sb, const uint8_t* ss, cons
 cudaError_t launch_residual_router(int T, int H, int E, const uint16_t* x, const uint16_t* y,
                                    const uint16_t* w_r, const uint16_t* b_r, uint16_t* x_out,
                                    float* logits, cudaStream_t st);
-// g_out = bf16(g + dx + d_logits W_r^T), fp32 arithmetic; g_out may alias g.
+// g_out = bf16(g + dx + d_logits W_r^T), fp32 arithmetic; g_out may alias g, dx may be null.
 cudaError_t launch_grad_chain(int T, int H, int E, const uint16_t* g, const uint16_t* dx,
                               const float* d_logits, const uint16_t* w_r, uint16_t* g_out,
                               cudaStream_t st);

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) grad_chain_kernel(
       if (t < T && h < H) {
         const size_t at = ((size_t)t * H + h) / 8;
         gv[r] = reinterpret_cast<const uint4*>(g)[at];
-        dv4[r] = __ldg(reinterpret_cast<const uint4*>(dx) + at);
+        if (dx) dv4[r] = __ldg(reinterpret_cast<const uint4*>(dx) + at);
       }
     }
     float acc[4][8];

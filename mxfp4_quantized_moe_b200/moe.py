@@ -202,12 +202,14 @@ def residual_router(x: torch.Tensor, y: torch.Tensor | None, w_r: torch.Tensor |
     return x_out, logits
 
 
-def grad_chain(g: torch.Tensor, dx: torch.Tensor, d_logits: torch.Tensor, w_r: torch.Tensor,
+def grad_chain(g: torch.Tensor, dx: torch.Tensor | None, d_logits: torch.Tensor, w_r: torch.Tensor,
                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """bf16(g + dx + d_logits W_r^T) in fp32, one kernel (out may be g itself)."""
+    """bf16(g + dx + d_logits W_r^T) in fp32, one kernel (out may be g itself; dx None: without
+    that term)."""
     T, H = g.shape
     E = w_r.shape[1]
-    if g.dtype != torch.bfloat16 or dx.shape != g.shape or dx.dtype != g.dtype:
+    if g.dtype != torch.bfloat16 or (dx is not None and (dx.shape != g.shape
+                                                         or dx.dtype != g.dtype)):
         raise ValueError("g and dx must be bf16 [T, H]")
     if d_logits.shape != (T, E) or d_logits.dtype != torch.float32:
         raise ValueError("d_logits must be fp32 [T, E]")

@@ -193,3 +193,9 @@ def test_wrappers_refuse_cpu_tensors_and_bad_names():
         moe.norm_forward(torch.zeros(3, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         moe.checkpoint_unpack(cp)
+
+
+def test_grad_chain_without_dx(L, reached):
+    gc = L.lib.mxfp4_moe_grad_chain
+    assert gc(4, 64, 8, A, None, B, C, D, None) in reached
+    assert gc(4, 64, 8, A, ODD, B, C, D, None) == L.ERR_INVALID_ARG
