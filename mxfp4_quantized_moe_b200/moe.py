@@ -231,29 +231,30 @@ _F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
 _ROWS = (torch.bfloat16, torch.float32)
 
 
-def _elsewhere(device: torch.device, stream):
-    """The context in which a call on `device` allocates and launches; None: the present one."""
-    if device.type != "cuda":
+def _elsewhere(t: torch.Tensor, stream):
+    """The context in which a call on t's device allocates and launches; None: the present one."""
+    if not t.is_cuda:
         raise ValueError("expected CUDA tensors")
     if stream is None:
-        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-    if stream.device != device:
+        here = t.get_device() == torch._C._cuda_getDevice()
+        return None if here else torch.cuda.device(t.device)
+    if stream.device != t.device:
         raise ValueError("stream and tensors are on different devices")
     return torch.cuda.stream(stream)
 
 
-def _current(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() costs 2 us more
+def _current(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)  # current_stream() costs 2 us more
 
 
-def _tensor(t: torch.Tensor, name: str, shape, dtypes, device) -> int:
-    """The data pointer of a dense tensor of that shape, type and device."""
+def _tensor(t: torch.Tensor, name: str, shape, dtypes, index: int) -> int:
+    """The data pointer of a dense tensor of that shape and type on CUDA device `index`."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:  # -1 on the host
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr() or _EMPTY
@@ -297,17 +298,17 @@ def route(routing: Routing, logits: torch.Tensor, bias: torch.Tensor | None = No
     expert.  Logits or biases of NaN, -inf or the lowest finite value mask an expert: it is
     selected last, with weight 0."""
     T, E = _logits_shape(logits)
-    dev = logits.device
-    where = _elsewhere(dev, stream)
+    where = _elsewhere(logits, stream)
     if where is not None:
         with where:
             return route(routing, logits, bias, topk_idx, topk_w, counts)
+    dev = logits.get_device()
     lp = _tensor(logits, "logits", (T, E), _F32, dev)
     bp = None if bias is None else _tensor(bias, "bias", (E,), _F32, dev)
     cp = None if counts is None else _tensor(counts, "counts", (E,), _I32, dev)
     dims, slots = routing.dims(T, E), (T, routing.k)
     if topk_idx is None:
-        topk_idx = torch.empty(slots, dtype=torch.int32, device=dev)
+        topk_idx = logits.new_empty(slots, dtype=torch.int32)
         ip = topk_idx.data_ptr() or _EMPTY
     else:
         ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
@@ -325,12 +326,12 @@ def route_backward(routing: Routing, logits: torch.Tensor, topk_idx: torch.Tenso
                    d_logits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """d_logits fp32 [T, E] from d_topk_w fp32 [T, k], for what `route` returned on `logits`."""
     T, E = _logits_shape(logits)
-    dev = logits.device
-    where = _elsewhere(dev, stream)
+    where = _elsewhere(logits, stream)
     if where is not None:
         with where:
             return route_backward(routing, logits, topk_idx, topk_w, d_topk_w, d_logits)
     slots = (T, routing.k)
+    dev = logits.get_device()
     lp = _tensor(logits, "logits", (T, E), _F32, dev)
     ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
     wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
@@ -351,17 +352,17 @@ def forward_routed(shape: MoeShape, w: dict, x: torch.Tensor, topk_idx: torch.Te
     """The block's forward on a given routing in place of its own (topk_idx int32 and topk_w fp32
     [T, k]).  `backward_input(..., want_d_logits=False)` follows it; its d_topk_w goes on to
     `route_backward`."""
-    dev = x.device
-    where = _elsewhere(dev, stream)
+    where = _elsewhere(x, stream)
     if where is not None:
         with where:
             return forward_routed(shape, w, x, topk_idx, topk_w, ws, y)
+    dev = x.get_device()
     rows, slots = (shape.T, shape.H), (shape.T, shape.k)
     xp = _tensor(x, "x", rows, (torch.bfloat16,), dev)
     ip = _tensor(topk_idx, "topk_idx", slots, _I32, dev)
     wp = _tensor(topk_w, "topk_w", slots, _F32, dev)
-    if ws.device != dev or any(t.device != dev for t in w.values()):
-        raise ValueError(f"ws and the weights must be on {dev}")
+    if ws.get_device() != dev or any(t.get_device() != dev for t in w.values()):
+        raise ValueError(f"ws and the weights must be on cuda:{dev}")
     if y is None:
         y = torch.empty_like(x)
     check(lib.mxfp4_moe_forward_routed(
@@ -385,7 +386,15 @@ class Checkpoint:
         return Checkpoint(torch.empty((T, H), dtype=torch.uint8, device=device),
                           torch.empty((T, H // 32), dtype=torch.uint8, device=device), format)
 
-    def _abi(self, T: int, H: int, device) -> _lib.Checkpoint:
+    @staticmethod
+    def _beside(x: torch.Tensor, format: str) -> "Checkpoint":
+        T, H = x.shape
+        if H % 32:
+            raise ValueError("a checkpoint needs H to be a multiple of 32")
+        return Checkpoint(x.new_empty((T, H), dtype=torch.uint8),
+                          x.new_empty((T, H // 32), dtype=torch.uint8), format)
+
+    def _abi(self, T: int, H: int, device: int) -> _lib.Checkpoint:
         if self.format not in _lib.CHECKPOINTS:
             raise ValueError(f"format must be one of {sorted(_lib.CHECKPOINTS)}")
         return _lib.Checkpoint(_tensor(self.codes, "codes", (T, H), _U8, device),
@@ -397,7 +406,7 @@ def _rows_shape(x):
     t = x.codes if isinstance(x, Checkpoint) else x
     if t.dim() != 2:
         raise ValueError("rows must be [T, H]")
-    return (*t.shape, t.device)
+    return (*t.shape, t)
 
 
 def _format(dtype: torch.dtype) -> int:
@@ -409,14 +418,15 @@ def _format(dtype: torch.dtype) -> int:
 def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | None = None,
                     stream=None) -> Checkpoint:
     """Rows [T, H] (bf16 or fp32, H a multiple of 32) stored in 8 bits."""
-    T, H, dev = _rows_shape(x)
-    where = _elsewhere(dev, stream)
+    T, H, t = _rows_shape(x)
+    where = _elsewhere(t, stream)
     if where is not None:
         with where:
             return checkpoint_pack(x, format, out)
+    dev = t.get_device()
     xp = _tensor(x, "x", (T, H), _ROWS, dev)
     if out is None:
-        out = Checkpoint.empty(T, H, format, dev)
+        out = Checkpoint._beside(x, format)
     check(lib.mxfp4_moe_checkpoint_pack(T, H, _format(x.dtype), xp, out._abi(T, H, dev),
                                         _current(dev)), "mxfp4_moe_checkpoint_pack")
     return out
@@ -425,15 +435,16 @@ def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | Non
 def checkpoint_unpack(checkpoint: Checkpoint, dtype: torch.dtype = torch.bfloat16,
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The rows [T, H] that a checkpoint stands for, as bf16 or fp32."""
-    T, H, dev = _rows_shape(checkpoint)
-    where = _elsewhere(dev, stream)
+    T, H, t = _rows_shape(checkpoint)
+    where = _elsewhere(t, stream)
     if where is not None:
         with where:
             return checkpoint_unpack(checkpoint, dtype, out)
+    dev = t.get_device()
     fmt = _format(dtype)
     frm = checkpoint._abi(T, H, dev)
     if out is None:
-        out = torch.empty((T, H), dtype=dtype, device=dev)
+        out = t.new_empty((T, H), dtype=dtype)
         op = out.data_ptr() or _EMPTY
     else:
         op = _tensor(out, "out", (T, H), (dtype,), dev)
@@ -477,7 +488,7 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
     x: bf16 or fp32 rows, or a Checkpoint (normalised as the rows it stands for, into `dtype`,
     bf16 by default).  y: a residual; x_out = x + y, rounded to the rows' type, is returned and
     is what is normalised.  checkpoint: a format or a Checkpoint to fill with those rows."""
-    T, H, dev = _rows_shape(x)
+    T, H, t = _rows_shape(x)
     stored = isinstance(x, Checkpoint)
     if stored:
         if y is not None or checkpoint is not None:
@@ -497,11 +508,12 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
     elif bias is not None:
         params = bias.dtype
     dims = _norm_dims(T, H, kind, eps, dtype, params)
-    where = _elsewhere(dev, stream)
+    where = _elsewhere(t, stream)
     if where is not None:
         with where:
             return norm_forward(x, weight, bias, kind=kind, eps=eps, y=y, checkpoint=checkpoint,
                                 dtype=dtype, out=out, x_out=x_out, mean=mean, rstd=rstd)
+    dev = t.get_device()
     rows, own = (T, H), (dtype,)
     xp = frm = yp = op = mp = to = None
     if stored:
@@ -519,15 +531,15 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
             op = _tensor(x_out, "x_out", rows, own, dev)
     if checkpoint is not None:
         if not isinstance(checkpoint, Checkpoint):
-            checkpoint = Checkpoint.empty(T, H, checkpoint, dev)
+            checkpoint = Checkpoint._beside(x, checkpoint)
         to = checkpoint._abi(T, H, dev)
     if out is None:
-        out = torch.empty(rows, dtype=dtype, device=dev) if stored else torch.empty_like(x)
+        out = t.new_empty(rows, dtype=dtype) if stored else torch.empty_like(x)
         np_ = out.data_ptr() or _EMPTY
     else:
         np_ = _tensor(out, "out", rows, own, dev)
     if rstd is None:
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        rstd = t.new_empty(T, dtype=torch.float32)
         rp = rstd.data_ptr() or _EMPTY
     else:
         rp = _tensor(rstd, "rstd", (T,), _F32, dev)
@@ -554,18 +566,19 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     be g itself).  params=False computes dx alone and returns None for the other two; d_bias is
     None for "rms" unless a tensor is given.  ws: scratch of norm_workspace_bytes (else
     allocated); two captured graphs that may run at once need one each."""
-    T, H, dev = _rows_shape(x)
+    T, H, t = _rows_shape(x)
     dtype = d_out.dtype
     dims = _norm_dims(T, H, kind, 0.0, dtype, dtype if weight is None else weight.dtype)
     if kind == "layer" and mean is None:
         raise ValueError("the layer norm's backward needs the mean")
     if not params and (d_weight is not None or d_bias is not None):
         raise ValueError("params=False with an output for the parameters' gradient")
-    where = _elsewhere(dev, stream)
+    where = _elsewhere(t, stream)
     if where is not None:
         with where:
             return norm_backward(d_out, x, mean, rstd, weight, kind=kind, g=g, params=params,
                                  dx=dx, d_weight=d_weight, d_bias=d_bias, ws=ws)
+    dev = t.get_device()
     rows, own = (T, H), (dtype,)
     xp = frm = dwp = dbp = wsp = None
     dp = _tensor(d_out, "d_out", rows, _ROWS, dev)
@@ -585,7 +598,7 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     ws_bytes = 0
     if params:
         if d_weight is None:
-            d_weight = torch.empty(H, dtype=torch.float32, device=dev)
+            d_weight = rstd.new_empty(H)
             dwp = d_weight.data_ptr()
         else:
             dwp = _tensor(d_weight, "d_weight", (H,), _F32, dev)
@@ -596,9 +609,9 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
             dbp = d_bias.data_ptr()
         if ws is None:
             ws_bytes = norm_workspace_bytes(T, H)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        elif ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"ws must be contiguous, on {dev}")
+            ws = t.new_empty(ws_bytes, dtype=torch.uint8)
+        elif ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous, on cuda:{dev}")
         else:
             ws_bytes = ws.numel() * ws.element_size()
         wsp = ws.data_ptr() or None
