@@ -409,15 +409,16 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   const bool live = row0 + tok < a.T;
   const long long row = live ? row0 + tok : a.T - 1;  // dead lanes repeat the last token
   const float* lg = a.logits + row * a.E;
-  const bool biased = a.bias != nullptr;
+  // keys are scores where a bias or a group's sum needs them, else the logits
+  const bool scored = a.bias != nullptr || (G != 1 && a.best2);
   // masked and missing experts hold the lowest finite value, below every other key; a token with
   // a logit of +inf is left to select()
   float x[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) x[i] = WHOLE || 8 * i + q < a.E ? __ldg(lg + 8 * i + q) : -FLT_MAX;
-  if (biased) {
+  if (scored) {
     for (int e = threadIdx.x; e < 8 * NS; e += blockDim.x)
-      s_bias[e] = e < a.E ? fminf(fmaxf(__ldg(a.bias + e), -FLT_MAX), FLT_MAX) : 0.f;
+      s_bias[e] = a.bias && e < a.E ? fminf(fmaxf(__ldg(a.bias + e), -FLT_MAX), FLT_MAX) : 0.f;
     __syncthreads();
   }
   if (row0 >= a.T) return;  // warp-uniform
@@ -425,7 +426,6 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   for (int i = 0; i < NS; ++i) x[i] = fmaxf(x[i], -FLT_MAX);
   // softmax statistics where scores or weights need them
   float top = 0.f, total = 1.f;
-  const bool scored = biased || (G != 1 && a.best2);
   if (!a.sigmoid && (scored || !a.renorm)) {
     float m = x[0];
 #pragma unroll
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_approx(-kLog2e * l)));
     return r;
   };
-  if (biased) {
+  if (scored) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       x[i] = x[i] > -FLT_MAX ? score(x[i]) + s_bias[8 * i + q] : -FLT_MAX;
@@ -456,7 +456,6 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   bool unsure = !(top < INFINITY);
   if constexpr (G != 1) {
     float mine = -FLT_MAX;  // lane q: score of group q
-    const bool from_scores = !biased && a.best2;
     int span = 0;
     float v1[G ? G : 1], v2[G ? G : 1];
     if constexpr (G > 1) {
@@ -466,8 +465,7 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
         v1[g] = v2[g] = -FLT_MAX;
 #pragma unroll
         for (int i = 0; i < kSpan; ++i) {
-          const float k = x[g * kSpan + i];
-          const float v = from_scores && k > -FLT_MAX ? score(k) : k;
+          const float v = x[g * kSpan + i];
           v2[g] = fmaxf(v2[g], fminf(v1[g], v));
           v1[g] = fmaxf(v1[g], v);
         }
@@ -501,7 +499,7 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         if (8 * i < a.E) {
-          const float v = from_scores && x[i] > -FLT_MAX ? score(x[i]) : x[i];
+          const float v = x[i];
           m2 = fmaxf(m2, fminf(m1, v));
           m1 = fmaxf(m1, v);
           if (--left == 0) {  // the group's two largest over the eight lanes
@@ -594,11 +592,11 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
   unsure |= last < (2u << 8);  // an expert out of the choice
   e = e < a.E ? e : 0;
   float l = fminf(__ldg(lg + e), FLT_MAX);
-  const float b = biased ? __ldg(a.bias + e) : 0.f;
+  const float b = a.bias ? __ldg(a.bias + e) : 0.f;
   {
     // places nearer than the keys' error (none for logits) need equal logits and biases
     const uint32_t near =
-        biased ? (uint32_t)fminf((unit_margin + 0x1p-22f * (fabsf(hi) + range)) * per, 8388607.f) + 1u : 0u;
+        scored ? (uint32_t)fminf((unit_margin + 0x1p-22f * (fabsf(hi) + range)) * per, 8388607.f) + 1u : 0u;
     const uint32_t below = __shfl_down_sync(kFull, mine, 1, 8);
     const float l1 = __shfl_down_sync(kFull, l, 1, 8), b1 = __shfl_down_sync(kFull, b, 1, 8);
     unsure |= q + 1 < a.k && (mine >> 8) - (below >> 8) <= near && !(l == l1 && b == b1);
@@ -613,7 +611,7 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
       for (int i = 0; i < NS; ++i)
         if (word[i] - reach < last - reach) {
           const int o = 8 * i + q;
-          unsure |= !(fminf(__ldg(lg + o), FLT_MAX) == lk && (!biased || __ldg(a.bias + o) == bk));
+          unsure |= !(fminf(__ldg(lg + o), FLT_MAX) == lk && (!a.bias || __ldg(a.bias + o) == bk));
         }
     }
   }
