@@ -741,6 +741,201 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
   }
 }
 
+// Rows that 16-byte vectors cannot read in place (H or a pointer without that alignment) are staged
+// whole, by the warps of the row together: the 16-byte pieces that begin inside the row by cp.async
+// (the last one with only its bytes of the row), what lies before the first of them by plain loads
+// of single features.  The row then stands at 16 - head bytes in its place, and a lane reads the
+// features lane, lane + 32, ... of every 256.
+template <int E>  // bytes of a feature
+struct LooseRow {
+  const uint8_t* from;
+  uint32_t head, bytes;  // bytes before the first piece; bytes of the row
+  MOE_DEV LooseRow(const void* base, size_t row, int H)
+      : from(static_cast<const uint8_t*>(base) + row * (size_t)((uint32_t)H * E)), bytes((uint32_t)H * E) {
+    head = min((16u - (uint32_t)(reinterpret_cast<uintptr_t>(from) & 15u)) & 15u, bytes);
+  }
+  static __host__ __device__ uint32_t place(int H) { return 16u + ((uint32_t)H * E + 15u) / 16u * 16u; }
+  // PIECES pieces a thread cover the row; returns the thread's feature of the head
+  template <int PIECES>
+  MOE_DEV uint32_t request(uint32_t to, int tid, int threads) const {
+    const uint32_t body = bytes - head;
+#pragma unroll
+    for (int c = 0; c < PIECES; ++c) {
+      const uint32_t off = 16u * (uint32_t)(tid + c * threads);
+      if (off < body)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16u + off),
+                     "l"(from + head + off), "r"(min(16u, body - off)) : "memory");
+    }
+    if ((uint32_t)tid * E >= head) return 0u;
+    if constexpr (E == 2) return reinterpret_cast<const uint16_t*>(from)[tid];
+    else return reinterpret_cast<const uint32_t*>(from)[tid];
+  }
+  MOE_DEV void put_head(uint32_t to, int tid, uint32_t feature) const {
+    if ((uint32_t)tid * E >= head) return;
+    const uint32_t at = to + 16u - head + (uint32_t)tid * E;
+    if constexpr (E == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)feature) : "memory");
+    else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(feature) : "memory");
+  }
+  // features h, h + 32, ... of which n lie in the row; 0 past its end
+  MOE_DEV void read(uint32_t to, int h, int n, float (&f)[8]) const {
+    const uint32_t at = to + 16u - head + (uint32_t)h * E;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t v = 0;
+      if constexpr (E == 2) {
+        uint16_t u = 0;
+        if (i < n) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at + 64u * i) : "memory");
+        v = (uint32_t)u << 16;
+      } else {
+        if (i < n) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + 128u * i) : "memory");
+      }
+      f[i] = __uint_as_float(v);
+    }
+  }
+};
+template <bool F32>
+MOE_DEV void store_loose(void* base, size_t row, int H, int h, int n, const float (&f)[8]) {
+  const size_t at = row * (size_t)(uint32_t)H + (uint32_t)h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) {
+      if constexpr (F32) static_cast<float*>(base)[at + 32 * i] = f[i];
+      else static_cast<uint16_t*>(base)[at + 32 * i] = f_to_bf16(f[i]);
+    }
+}
+// n features from h on, 32 apart, of a parameter; 0 past the end
+MOE_DEV void loose_params(const void* base, bool f32, int h, int n, float absent, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[1] = {0.f};
+    if (i < n) load_params<1>(base, f32, h + 32 * i, absent, v);
+    f[i] = v[0];
+  }
+}
+MOE_DEV int loose_count(int H, int h) { return max(0, min(8, (H - h + 31) / 32)); }
+
+template <int SRC, bool F32, bool RES, int NC, int RB, int NT, int BLOCKS>
+__global__ void __launch_bounds__(NT, BLOCKS) norm_forward_loose_kernel(NormArgs a, int W) {
+  constexpr int V = 8, E = F32 ? 4 : 2, kPieces = NC * E / 2 + 1, kSets = RES ? 2 : 1;
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // per group: 2 turns x RB rows x (x, y)
+  __shared__ float s_buf[NT / 32][2][2][RB * (NT / 32)];
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
+  const int G = blockDim.x / (32 * W), tid = wi * 32 + lane;
+  const uint32_t place = LooseRow<E>::place(a.H);
+  const uint32_t base = smem_u32(s_dyn) + (uint32_t)group * (2 * RB * kSets) * place;
+  const float inv_h = 1.f / (float)a.H;
+  int h[NC], n[NC];
+  Vals<V> pg[NC], pb[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    h[c] = 256 * (wi * NC + c) + lane;
+    n[c] = loose_count(a.H, h[c]);
+    float f[V];
+    loose_params(a.weight, a.param_f32, h[c], n[c], 1.f, f);
+    set<V>(pg[c], f);
+    loose_params(a.bias, a.param_f32, h[c], n[c], 0.f, f);
+    set<V>(pb[c], f);
+  }
+  const uint32_t rows = (uint32_t)a.T;  // rows past the last one stand for it
+  uint32_t hx[RB], hy[RES ? RB : 1];
+  auto spot = [&](int turn, int j, int set) { return base + (uint32_t)((turn * RB + j) * kSets + set) * place; };
+  auto request = [&](uint32_t row, int turn) {
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const size_t r = min(row + j, rows - 1);
+      hx[j] = LooseRow<E>(a.x, r, a.H).template request<kPieces>(spot(turn, j, 0), tid, 32 * W);
+      if constexpr (RES)
+        hy[j] = LooseRow<E>(a.y, r, a.H).template request<kPieces>(spot(turn, j, 1), tid, 32 * W);
+    }
+    copy_async_commit();
+  };
+  const uint32_t step = gridDim.x * (uint32_t)(G * RB);
+  uint32_t row = (blockIdx.x * (uint32_t)G + group) * RB;
+  if (row < rows) request(row, 0);
+  int turn = 0;
+  for (; row < rows; row += step) {
+    Vals<V> v[RB][NC];
+    copy_async_wait<0>();
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const size_t r = min(row + j, rows - 1);
+      LooseRow<E>(a.x, r, a.H).put_head(spot(turn, j, 0), tid, hx[j]);
+      if constexpr (RES) LooseRow<E>(a.y, r, a.H).put_head(spot(turn, j, 1), tid, hy[j]);
+    }
+    // the rows have arrived, and every lane is done with the other turn's places
+    if (W > 1) group_barrier(1 + group, W); else __syncwarp();
+    if (rows - row > step) request(row + step, turn ^ 1);
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const size_t r = min(row + j, rows - 1);
+      const LooseRow<E> lx(a.x, r, a.H);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float f[V];
+        lx.read(spot(turn, j, 0), h[c], n[c], f);
+        if constexpr (RES) {
+          float u[V];
+          LooseRow<E>(a.y, r, a.H).read(spot(turn, j, 1), h[c], n[c], u);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            f[i] += u[i];
+            if constexpr (!F32) f[i] = bf16_to_f(f_to_bf16(f[i]));
+          }
+          store_loose<F32>(a.x_out, r, a.H, h[c], n[c], f);
+        }
+        set<V>(v[j][c], f);
+      }
+    }
+    float mean[RB], q[RB];
+#pragma unroll
+    for (int j = 0; j < RB; ++j) mean[j] = 0.f;
+    if (!a.rms) {
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        Pair t;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) add_sum<V>(t, v[j][c]);
+        mean[j] = t.sum();
+      }
+      group_totals<RB>(mean, W, wi, 1 + group, s_buf[group][turn][0]);
+    }
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      mean[j] *= inv_h;
+      q[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float f[V];
+        get<V>(v[j][c], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = i < n[c] ? f[i] - mean[j] : 0.f;
+        set<V>(v[j][c], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[j] = fmaf(f[i], f[i], q[j]);
+      }
+    }
+    group_totals<RB>(q, W, wi, 1 + group, s_buf[group][turn][1]);
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const uint32_t r = min(row + j, rows - 1);
+      q[j] = rsqrtf(q[j] * inv_h + a.eps);
+      if (wi == 0 && lane == 0) {
+        if (a.mean) a.mean[r] = mean[j];
+        if (a.rstd) a.rstd[r] = q[j];
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        scale_shift<V>(v[j][c], q[j], pg[c], pb[c]);
+        float f[V];
+        get<V>(v[j][c], f);
+        store_loose<F32>(a.out, r, a.H, h[c], n[c], f);
+      }
+    }
+    turn ^= 1;
+  }
+}
+
 // ---- backward -------------------------------------------------------------------------------
 // A thread keeps the same features (V NC of them) over all rows of its block, so the parameters'
 // gradients accumulate in its registers and leave once per block; a second kernel adds the
@@ -1128,9 +1323,160 @@ __global__ void __launch_bounds__(NT, BLOCKS)
   }
 }
 
+// The staged form for rows without vector alignment (see LooseRow): x, d_out and g of a turn are
+// requested together, into the other of two places.
+template <bool F32, bool HASG, int NC, int R, int NT, int BLOCKS>
+__global__ void __launch_bounds__(NT, BLOCKS)
+    norm_backward_loose_kernel(NormGradArgs a, int W, int rows_per_block) {
+  constexpr int V = 8, Q = 2 * R, E = F32 ? 4 : 2, kPieces = NC * E / 2 + 1, kSets = HASG ? 3 : 2;
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // per group: 2 turns x R rows x (x, d_out, g)
+  __shared__ float s_buf[NT / 32][2][Q * (NT / 32)];
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int group = W == 1 ? warp : warp / W, wi = W == 1 ? 0 : warp % W;
+  const int G = blockDim.x / (32 * W), tid = wi * 32 + lane;
+  const uint32_t place = LooseRow<E>::place(a.H);
+  const uint32_t base = smem_u32(s_dyn) + (uint32_t)group * (2 * R * kSets) * place;
+  const float inv_h = 1.f / (float)a.H;
+  int h[NC], n[NC];
+  Vals<V> acc_g[NC], acc_b[NC], pg[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    h[c] = 256 * (wi * NC + c) + lane;
+    n[c] = loose_count(a.H, h[c]);
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = 0.f;
+    set<V>(acc_g[c], f);
+    set<V>(acc_b[c], f);
+    loose_params(a.weight, a.param_f32, h[c], n[c], 1.f, f);
+    set<V>(pg[c], f);
+  }
+  const uint32_t begin = blockIdx.x * (uint32_t)rows_per_block;
+  const uint32_t end = min((uint32_t)a.T, begin + (uint32_t)rows_per_block);
+  auto spot = [&](int turn, int j, int set) { return base + (uint32_t)((turn * R + j) * kSets + set) * place; };
+  uint32_t head[kSets][R];
+  float mean_next[R], rstd_next[R];
+  const void* from[3] = {a.x, a.d_out, a.g};
+  auto request = [&](uint32_t row, int turn) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const uint32_t r = min(row + j, end - 1);
+#pragma unroll
+      for (int t = 0; t < kSets; ++t)
+        head[t][j] = LooseRow<E>(from[t], r, a.H).template request<kPieces>(spot(turn, j, t), tid, 32 * W);
+      mean_next[j] = a.rms ? 0.f : __ldg(a.mean + r);
+      rstd_next[j] = __ldg(a.rstd + r);
+    }
+    copy_async_commit();
+  };
+  const uint32_t step = (uint32_t)(G * R);
+  uint32_t row = begin + (uint32_t)(group * R);
+  if (row < end) request(row, 0);
+  int turn = 0;
+  for (; row < end; row += step) {
+    float mean[R], rstd[R];
+    copy_async_wait<0>();
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const uint32_t r = min(row + j, end - 1);
+      mean[j] = mean_next[j];
+      rstd[j] = rstd_next[j];
+#pragma unroll
+      for (int t = 0; t < kSets; ++t)
+        LooseRow<E>(from[t], r, a.H).put_head(spot(turn, j, t), tid, head[t][j]);
+    }
+    // the rows have arrived, and every lane is done with the other turn's places
+    if (W > 1) group_barrier(1 + group, W); else __syncwarp();
+    if (end - row > step) request(row + step, turn ^ 1);
+    Vals<V> xh[R][NC], v[R][NC];
+    float q[Q];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const uint32_t r = min(row + j, end - 1);
+      const bool live = row + j < end;  // a row past the block's last one counts for nothing
+      Pair c1, c2;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float f[V];
+        LooseRow<E>(a.x, r, a.H).read(spot(turn, j, 0), h[c], n[c], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = i < n[c] ? (f[i] - mean[j]) * rstd[j] : 0.f;
+        set<V>(xh[j][c], f);
+        LooseRow<E>(a.d_out, r, a.H).read(spot(turn, j, 1), h[c], live ? n[c] : 0, f);
+        set<V>(v[j][c], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t d = v[j][c].p[i];
+          acc_g[c].p[i] = f2fma(d, xh[j][c].p[i], acc_g[c].p[i]);
+          acc_b[c].p[i] = f2add(acc_b[c].p[i], d);
+          v[j][c].p[i] = f2mul(d, pg[c].p[i]);
+          c1.p = f2add(c1.p, v[j][c].p[i]);
+          c2.p = f2fma(v[j][c].p[i], xh[j][c].p[i], c2.p);
+        }
+      }
+      q[2 * j] = a.rms ? 0.f : c1.sum();
+      q[2 * j + 1] = c2.sum();
+    }
+    group_totals<Q>(q, W, wi, 1 + group, s_buf[group][turn]);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const uint32_t r = min(row + j, end - 1);
+      const float k1 = -rstd[j] * (q[2 * j] * inv_h), k2 = -rstd[j] * (q[2 * j + 1] * inv_h);
+      const uint64_t p1 = f2(k1, k1), p2 = f2(k2, k2), r2 = f2(rstd[j], rstd[j]);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[j][c].p[i] = f2fma(v[j][c].p[i], r2, f2fma(xh[j][c].p[i], p2, p1));
+        float f[V];
+        get<V>(v[j][c], f);
+        if constexpr (HASG) {
+          float g[V];
+          LooseRow<E>(a.g, r, a.H).read(spot(turn, j, 2), h[c], n[c], g);
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[i] += g[i];
+        }
+        store_loose<F32>(a.dx, r, a.H, h[c], row + j < end ? n[c] : 0, f);
+      }
+    }
+    turn ^= 1;
+  }
+  if (!a.d_weight && !a.d_bias) return;
+  launch_dependents();
+  // the block's sum over its groups, in group order, to its row of the partial sums
+  __syncthreads();
+  float* s_sum = reinterpret_cast<float*>(s_dyn);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float* part = partial_row(a, which);
+    if (!part) continue;
+    const Vals<V>* acc = which ? acc_b : acc_g;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float f[V];
+      get<V>(acc[c], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n[c]) {
+          if (G > 1) s_sum[(size_t)group * a.H + h[c] + 32 * i] = f[i];
+          else part[h[c] + 32 * i] = f[i];
+        }
+    }
+    if (G > 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
+        float t = 0.f;
+        for (int g = 0; g < G; ++g) t += s_sum[(size_t)g * a.H + i];
+        part[i] = t;
+      }
+      __syncthreads();
+    }
+  }
+}
+
 // d_weight (blockIdx.y 0) and d_bias (1) from the blocks' partial sums: 32 features per block,
 // its warps over the parts.
-constexpr int kReduceWarps = 16;
+constexpr int kReduceWarps = 16;  // most; fewer parts take fewer
 __global__ void __launch_bounds__(32 * kReduceWarps) norm_reduce_kernel(
     const float* __restrict__ partial, int parts, int H, float* __restrict__ d_weight,
     float* __restrict__ d_bias) {
@@ -1144,13 +1490,12 @@ __global__ void __launch_bounds__(32 * kReduceWarps) norm_reduce_kernel(
   if (h < H) {
     const float* p = partial + (size_t)blockIdx.y * H + h;
 #pragma unroll 8
-    for (int i = warp; i < parts; i += kReduceWarps) v += p[(size_t)i * 2 * H];
+    for (int i = warp; i < parts; i += blockDim.x >> 5) v += p[(size_t)i * 2 * H];
   }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && h < H) {
-#pragma unroll
-    for (int i = 1; i < kReduceWarps; ++i) v += s[i][lane];
+    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v += s[i][lane];
     out[h] = v;
   }
 }
@@ -1229,6 +1574,23 @@ cudaError_t forward_persistent(const NormArgs& a, int W, int sms, cudaStream_t s
   kern<<<(unsigned)(need < most ? need : most), 32 * W * groups, smem, st>>>(a, W);
   return cudaGetLastError();
 }
+template <bool F32, bool RES, int NC, int RB, int NT, int BLOCKS>
+cudaError_t forward_loose(const NormArgs& a, int W, int sms, cudaStream_t st) {
+  auto kern = norm_forward_loose_kernel<F32 ? kF32 : kBf16, F32, RES, NC, RB, NT, BLOCKS>;
+  const int groups = NT / (32 * W);
+  const int smem = groups * 2 * RB * (RES ? 2 : 1) * (int)LooseRow<F32 ? 4 : 2>::place(a.H);
+  const cudaError_t e = allow_shared(kern, smem);
+  if (e != cudaSuccess) return e;
+  const long long need = ((long long)a.T + RB * groups - 1) / (RB * groups);
+  const long long most = (long long)sms * BLOCKS;
+  kern<<<(unsigned)(need < most ? need : most), 32 * W * groups, smem, st>>>(a, W);
+  return cudaGetLastError();
+}
+template <bool F32, int NC, int RB, int NT, int BLOCKS>
+cudaError_t forward_loose_pick(const NormArgs& a, int W, int sms, cudaStream_t st) {
+  return a.y ? forward_loose<F32, true, NC, RB, NT, BLOCKS>(a, W, sms, st)
+             : forward_loose<F32, false, NC, RB, NT, BLOCKS>(a, W, sms, st);
+}
 template <int SRC, bool F32, int NC, int RB, int NT, int BLOCKS>
 cudaError_t forward_many(const NormArgs& a, int W, int sms, cudaStream_t st) {
   if constexpr (SRC == kBf16 || SRC == kF32)
@@ -1259,6 +1621,12 @@ cudaError_t forward_from(const NormArgs& a, bool vec, int sms, cudaStream_t st) 
     return forward_launch<SRC, F32, 8, 4, 1>(a, warps(4), st);
   }
   if constexpr (SRC == kBf16 || SRC == kF32) {
+    if (a.T >= kManyRows && a.H <= 8192) {
+      const int W1 = (a.H + 255) / 256;
+      if (W1 <= 12) return forward_loose_pick<F32, 1, F32 ? 2 : 4, 384, 2>(a, W1, sms, st);
+      if (W1 <= 16) return forward_loose_pick<F32, 1, F32 ? 1 : 2, 512, 2>(a, W1, sms, st);
+      return forward_loose_pick<F32, 2, 1, 512, 1>(a, (a.H + 511) / 512, sms, st);
+    }
     if (a.H <= 4096) return forward_launch<SRC, F32, 1, 8, 1>(a, (a.H + 255) / 256, st);
     return forward_launch<SRC, F32, 1, 32, 1>(a, (a.H + 1023) / 1024, st);
   }
@@ -1304,6 +1672,21 @@ cudaError_t backward_staged(const NormGradArgs& a, int W, int* parts, cudaStream
   return cudaGetLastError();
 }
 
+template <bool F32, bool HASG, int NC, int R, int NT, int BLOCKS>
+cudaError_t backward_loose(const NormGradArgs& a, int W, int* parts, cudaStream_t st) {
+  auto kern = norm_backward_loose_kernel<F32, HASG, NC, R, NT, BLOCKS>;
+  const int groups = NT / (32 * W);
+  int smem = groups * 2 * R * (HASG ? 3 : 2) * (int)LooseRow<F32 ? 4 : 2>::place(a.H);
+  const int sums = 4 * a.H * groups;  // the groups' sums at the end
+  if (smem < sums) smem = sums;
+  const cudaError_t e = allow_shared(kern, smem);
+  if (e != cudaSuccess) return e;
+  const Share sh = share_rows(a.T, R * groups, BLOCKS);
+  *parts = sh.blocks;
+  kern<<<sh.blocks, 32 * W * groups, smem, st>>>(a, W, sh.rows);
+  return cudaGetLastError();
+}
+
 template <int SRC, bool F32, bool HASG>
 cudaError_t backward_from(const NormGradArgs& a, bool vec, int* parts, cudaStream_t st) {
   if (vec) {
@@ -1314,9 +1697,10 @@ cudaError_t backward_from(const NormGradArgs& a, bool vec, int* parts, cudaStrea
     return backward_launch<SRC, F32, 8, 4, 1, HASG, 512, 1>(a, (a.H + 1023) / 1024, parts, st);
   }
   if constexpr (SRC == kBf16 || SRC == kF32) {
-    const int W8 = (a.H + 255) / 256, W16 = (a.H + 511) / 512;
-    if (W8 <= 12) return backward_launch<SRC, F32, 1, 8, 1, HASG, 384, 2>(a, W8, parts, st);
-    if (W16 <= 16) return backward_launch<SRC, F32, 1, 16, 1, HASG, 512, 1>(a, W16, parts, st);
+    const int W1 = (a.H + 255) / 256;
+    if (W1 <= 12) return backward_loose<F32, HASG, 1, F32 ? 1 : 2, 384, 2>(a, W1, parts, st);
+    if (W1 <= 16) return backward_loose<F32, HASG, 1, F32 ? 1 : 2, 512, 1>(a, W1, parts, st);
+    if (W1 <= 32) return backward_loose<F32, HASG, 2, 1, 512, 1>(a, (a.H + 511) / 512, parts, st);
     return backward_launch<SRC, F32, 1, 32, 1, HASG, 512, 1>(a, (a.H + 1023) / 1024, parts, st);
   }
   return cudaErrorInvalidValue;  // checkpoints are aligned
@@ -1367,7 +1751,7 @@ cudaError_t launch_norm_backward(const NormGradArgs& a, int, cudaStream_t st) {
   if (parts == 1) return cudaSuccess;  // one block writes the gradients itself
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((a.H + 31) / 32, 2);
-  cfg.blockDim = dim3(32 * kReduceWarps);
+  cfg.blockDim = dim3(parts >= 64 ? 32 * kReduceWarps : 256);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

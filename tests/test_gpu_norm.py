@@ -90,7 +90,10 @@ def check_backward(dx, dw, db, d_out, x, w, kind, dtype, g=None, eps=1e-5):
 
 
 SHAPES = [(1, 1), (1, 2880), (3, 7), (5, 33), (2, 64), (17, 96), (700, 256), (9, 1000), (4, 1001),
-          (300, 2880), (1203, 520), (3, 4096), (2, 8192), (3, 12000), (5, 16384), (2, 16383)]
+          (300, 2880), (1203, 520), (3, 4096), (2, 8192), (3, 12000), (5, 16384), (2, 16383),
+          # many rows: the persistent forms, of whole vectors and of any length
+          (1301, 32), (1500, 2880), (620, 4096), (601, 8192), (600, 16384), (2000, 1), (1400, 7),
+          (650, 61), (900, 255), (610, 1001), (640, 2879), (603, 4099), (601, 7001), (600, 12001)]
 
 
 @pytest.mark.parametrize("kind", ["layer", "rms"])
@@ -246,11 +249,12 @@ def test_in_place_gradient_and_outputs_of_the_caller(moe):
     assert torch.equal(out[:T], dx) and (out[T:] == 9).all()
 
 
-@pytest.mark.parametrize("H", [64, 61])
+@pytest.mark.parametrize("T", [19, 700])
+@pytest.mark.parametrize("H", [64, 61, 512])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_rows_without_vector_alignment(moe, H, dtype):
+def test_rows_without_vector_alignment(moe, H, dtype, T):
     """Views that begin at any element give the same values as aligned copies."""
-    T, dt = 19, TYPES[dtype]
+    dt = TYPES[dtype]
     base = [rows(1, T * H + 8, dt, s)[0].cuda() for s in range(4)]
     for off in (1, 2, 4):
         x, y, d, g = (t[off:off + T * H].view(T, H) for t in base)
