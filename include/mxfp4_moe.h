@@ -305,7 +305,7 @@ MXFP4_MOE_API int mxfp4_moe_grad_chain(int32_t T, int32_t H, int32_t E, const ui
  *             expert, so a token whose every expert is masked gets k zero weights.
  * T >= 0, 1 <= k <= E <= 256, 1 <= groups <= 32 dividing E, 1 <= top_groups <= groups with
  * top_groups * E / groups >= k, group_best 1 or 2 (2 only with E / groups >= 2; ignored with
- * groups == 1), scale finite and not 0. */
+ * groups == 1), scale a normal number (not 0). */
 #define MXFP4_MOE_SCORES_SOFTMAX 0
 #define MXFP4_MOE_SCORES_SIGMOID 1
 typedef struct {
@@ -396,8 +396,9 @@ MXFP4_MOE_API int mxfp4_moe_checkpoint_unpack(int32_t T, int32_t H, int32_t rows
  *   out = (x - mean) rstd weight + bias
  * T >= 0, 1 <= H <= 16384, eps finite and >= 0.  Rows (x, y, x_out, out, d_out, g, dx) have
  * type rows_format and are dense; weight and bias [H] have type param_format.  Pointers are
- * aligned to their element type at least; 16-byte aligned pointers with H a multiple of 8 take
- * the vector path. */
+ * aligned to their element type at least; with a checkpoint, rows, weight and bias are 16-byte
+ * aligned.  Rows and parameters that are, with H a multiple of 8, are read in place; others go
+ * through shared memory at about half the speed. */
 #define MXFP4_MOE_NORM_LAYER 0
 #define MXFP4_MOE_NORM_RMS 1
 typedef struct {

@@ -268,7 +268,7 @@ int check_routing(const mxfp4_moe_routing* r) {
     return MXFP4_MOE_ERR_INVALID_ARG;
   if (r->group_best != 1 && r->group_best != 2) return MXFP4_MOE_ERR_INVALID_ARG;
   if (r->groups > 1 && r->group_best > r->E / r->groups) return MXFP4_MOE_ERR_INVALID_ARG;
-  if (!std::isfinite(r->scale) || r->scale == 0.f) return MXFP4_MOE_ERR_INVALID_ARG;
+  if (!std::isnormal(r->scale)) return MXFP4_MOE_ERR_INVALID_ARG;
   return MXFP4_MOE_OK;
 }
 

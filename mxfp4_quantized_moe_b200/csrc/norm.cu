@@ -1313,10 +1313,9 @@ __global__ void __launch_bounds__(NT, BLOCKS)
       for (int c = 0; c < NC; ++c) {
         float f[V];
         get<V>(acc[c], f);
-        if (in[c]) {
-          float4* to = reinterpret_cast<float4*>(part + h0 + 256 * c);
-          to[0] = make_float4(f[0], f[1], f[2], f[3]);
-          to[1] = make_float4(f[4], f[5], f[6], f[7]);
+        if (in[c]) {  // by single features: a caller's gradient is aligned to one
+#pragma unroll
+          for (int i = 0; i < V; ++i) part[h0 + 256 * c + i] = f[i];
         }
       }
     }

@@ -50,7 +50,7 @@ GOOD = dict(T=4, E=16, k=4, scores=0, groups=4, top_groups=2, group_best=2, reno
     dict(scores=-1), dict(groups=0), dict(groups=3), dict(groups=64), dict(top_groups=0),
     dict(top_groups=5), dict(top_groups=1, k=5), dict(group_best=0), dict(group_best=3),
     dict(groups=16, top_groups=4, group_best=2), dict(scale=0.0), dict(scale=float("nan")),
-    dict(scale=float("inf"))])
+    dict(scale=float("inf")), dict(scale=1e-40)])
 def test_routing_refusals(L, bad):
     r = L.Routing(*(dict(GOOD, **bad)[n] for n, _ in L.Routing._fields_))
     assert L.lib.mxfp4_moe_route(r, A, None, B, C, None, None) == L.ERR_INVALID_ARG

@@ -267,6 +267,25 @@ def test_rows_without_vector_alignment(moe, H, dtype, T):
         check_backward(dx, dw, db, f64(d), f64(a.x_out), f64(w), "layer", dt, f64(g))
 
 
+@pytest.mark.parametrize("T", [1, 2, 5, 400])
+def test_parameter_gradients_at_any_address(moe, T):
+    """Outputs of the parameters' gradients that begin at any fp32 element."""
+    H = 320
+    x, d = rows(T, H, torch.bfloat16, 1).cuda(), rows(T, H, torch.bfloat16, 2).cuda()
+    f = moe.norm_forward(x)
+    _, dw, db = moe.norm_backward(d, x, f.mean, f.rstd)
+    base = torch.full((2, H + 4), 5.0, device="cuda")
+    for off in (1, 2, 3):
+        a, b = base[0, off:off + H], base[1, off:off + H]
+        moe.norm_backward(d, x, f.mean, f.rstd, d_weight=a, d_bias=b)
+        assert torch.equal(a, dw) and torch.equal(b, db)
+        assert base[:, :1].eq(5).all()
+        cp = moe.checkpoint_pack(x)
+        n = moe.norm_forward(cp)
+        moe.norm_backward(d, cp, n.mean, n.rstd, d_weight=a, d_bias=b)
+        assert torch.isfinite(a).all() and torch.equal(b, db)
+
+
 def test_empty_batch(moe):
     for dt in TYPES.values():
         x = torch.empty(0, 64, dtype=dt, device="cuda")
