@@ -9,7 +9,10 @@
   per-kernel event timing: the forward gather (`gather_x`: A rows of H bf16 read and
   written), the combines
   (`combine_y`, `combine_dx`: A rows read, T rows written) and the dY gather with the
-  routing-weight dot (`gather_dy_dw`: A rows of dY and of y read, A rows written).
+  routing-weight dot (`gather_dy_dw`: A rows of dY and of y read, A rows written);
+* the operators at the block's edge at the stack's size, T=32768, H=2880 (each through its own
+  entry point): the norm's forward and backward with the residual stream and from an 8-bit
+  checkpoint, the checkpoint alone, and the routing of 256 experts with its gradient.
 
 Prints one JSON line per stage with its algorithmic bytes, time and GB/s against the HBM copy
 bandwidth in MEASURED_PEAKS.json (or the fallback figure).
@@ -95,6 +98,61 @@ def main():
                           "gbs": nbytes / (ms / 1e3) / 1e9,
                           "frac_of_hbm": nbytes / (ms / 1e3) / 1e9 / peak,
                           "peak_gbs": peak, "peak_source": src}), flush=True)
+    del w, wt, x, lg, dy, ws, y
+    torch.cuda.empty_cache()
+    edge(args.iters, peak, src)
+
+
+def edge(iters, peak, src):
+    """The operators at the block's edge; inputs of several hundred MB, past L2."""
+    T, H, E, k = 32768, 2880, 256, 8
+    x, y, d, g = (torch.randn(T, H, device="cuda").bfloat16() for _ in range(4))
+    weight = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    f = moe.norm_forward(x, weight, weight, y=y, checkpoint="e4m3")
+    cp, dx = f.checkpoint, torch.empty_like(x)
+    ws = torch.empty(moe.norm_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+    grads = dict(dx=dx, d_weight=torch.empty(H, device="cuda"), d_bias=torch.empty(H, device="cuda"),
+                 ws=ws)
+    outs = dict(out=f.out, mean=f.mean, rstd=f.rstd)
+    logits = torch.randn(T, E, device="cuda")
+    r = moe.Routing(k, "sigmoid", 8, 4, 2)
+    idx, w = moe.route(r, logits)
+    dl, cells, packed = torch.empty_like(logits), T * H, 1 + 1 / 32
+    stages = (
+        ("norm_forward", cells * 4.0, lambda: moe.norm_forward(x, weight, weight, **outs)),
+        ("norm_forward_residual", cells * 8.0,
+         lambda: moe.norm_forward(x, weight, weight, y=y, x_out=f.x_out, **outs)),
+        ("norm_forward_residual_checkpoint", cells * (8.0 + packed),
+         lambda: moe.norm_forward(x, weight, weight, y=y, x_out=f.x_out, checkpoint=cp, **outs)),
+        ("norm_forward_from_checkpoint", cells * (2.0 + packed),
+         lambda: moe.norm_forward(cp, weight, weight, **outs)),
+        ("norm_backward", cells * 6.0,
+         lambda: moe.norm_backward(d, x, f.mean, f.rstd, weight, **grads)),
+        ("norm_backward_residual", cells * 8.0,
+         lambda: moe.norm_backward(d, x, f.mean, f.rstd, weight, g=g, **grads)),
+        ("norm_backward_residual_from_checkpoint", cells * (6.0 + packed),
+         lambda: moe.norm_backward(d, cp, f.mean, f.rstd, weight, g=g, **grads)),
+        ("checkpoint_pack", cells * (2.0 + packed), lambda: moe.checkpoint_pack(x, out=cp)),
+        ("checkpoint_unpack", cells * (2.0 + packed), lambda: moe.checkpoint_unpack(cp, out=dx)),
+        ("route", T * (4.0 * E + 8 * k), lambda: moe.route(r, logits, None, idx, w)),
+        ("route_backward", T * (4.0 * E + 12 * k),
+         lambda: moe.route_backward(r, logits, idx, w, w, dl)),
+    )
+    for name, nbytes, call in stages:
+        for _ in range(3):
+            call()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        e0.record()
+        for _ in range(iters):
+            call()
+        e1.record()
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / iters
+        gbs = nbytes / (ms / 1e3) / 1e9
+        print(json.dumps({"stage": name, "bytes": nbytes, "ms": ms, "gbs": gbs,
+                          "frac_of_hbm": gbs / peak, "peak_gbs": peak, "peak_source": src}),
+              flush=True)
 
 
 if __name__ == "__main__":

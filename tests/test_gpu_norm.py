@@ -286,6 +286,26 @@ def test_parameter_gradients_at_any_address(moe, T):
         assert torch.isfinite(a).all() and torch.equal(b, db)
 
 
+@pytest.mark.parametrize("H", [8192, 8189])
+def test_rows_past_32_bit_offsets(moe, H):
+    """Rows of more than 2^31 elements: the last ones as in a batch of their own."""
+    T, n = 2 ** 31 // H + 700, 650
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_()
+    tail = x[-n:].clone()
+    f, t = moe.norm_forward(x), moe.norm_forward(tail)
+    assert torch.equal(f.out[-n:], t.out) and torch.equal(f.rstd[-n:], t.rstd)
+    dx, _, _ = moe.norm_backward(f.out, x, f.mean, f.rstd)
+    dt, _, _ = moe.norm_backward(t.out, tail, t.mean, t.rstd)
+    assert torch.equal(dx[-n:], dt)
+    if H % 32 == 0:
+        cp = moe.checkpoint_pack(x, "int8")
+        ct = moe.checkpoint_pack(tail, "int8")
+        assert torch.equal(cp.codes[-n:], ct.codes) and torch.equal(cp.scales[-n:], ct.scales)
+        assert torch.equal(moe.checkpoint_unpack(cp)[-n:], moe.checkpoint_unpack(ct))
+        again = moe.norm_forward(cp)
+        assert torch.equal(again.out[-n:], moe.norm_forward(ct).out)
+
+
 def test_empty_batch(moe):
     for dt in TYPES.values():
         x = torch.empty(0, 64, dtype=dt, device="cuda")

@@ -191,6 +191,41 @@ def test_backward_takes_any_slots(moe):
             np.testing.assert_allclose(d.double().cpu().numpy(), ref.numpy(), rtol=2e-6, atol=2e-6)
 
 
+@pytest.mark.parametrize("k", [7, 12, 40])
+def test_backward_adds_repeated_slots_in_order(moe, k):
+    """Rows that name few experts many times: the same bits every time, the sum of the slots."""
+    T, E = 33, 48
+    gen = torch.Generator().manual_seed(k)
+    logits, dw = normal(T, E, 1), normal(T, k, 2)
+    idx = torch.randint(0, 3, (T, k), generator=gen, dtype=torch.int32) * 7
+    w = torch.rand(T, k, generator=gen)
+    r = moe.Routing(k, "softmax")
+    args = (r, logits.cuda(), idx.cuda(), w.cuda(), dw.cuda())
+    d = moe.route_backward(*args)
+    assert all(torch.equal(d, moe.route_backward(*args)) for _ in range(3))
+    q = w.double() * (dw.double() - (w.double() * dw.double()).sum(1, keepdim=True))
+    ref = torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, idx.long(), q)
+    mag = torch.zeros(T, E, dtype=torch.float64).scatter_add_(
+        1, idx.long(), w.double() * (dw.double().abs() + (w * dw).double().abs().sum(1, keepdim=True)))
+    # products, the dot over k terms and the sum of at most k slots, each rounded once
+    assert ((d.double().cpu() - ref).abs() <= (2 * k + 8) * R * mag + 1e-30).all()
+
+
+def test_rows_past_32_bit_offsets(moe):
+    """Logits of more than 2^31 elements: the last tokens as in a batch of their own."""
+    E, k = 256, 4
+    T = 2 ** 31 // E + 1000
+    logits = torch.empty(T, E, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    r = moe.Routing(k, "softmax", renormalize=False)
+    idx, w = moe.route(r, logits)
+    tail = logits[-999:].clone()
+    i2, w2 = moe.route(r, tail)
+    assert torch.equal(idx[-999:], i2) and torch.equal(w[-999:], w2)
+    dw = torch.ones(T, k, device="cuda")
+    d = moe.route_backward(r, logits, idx, w, dw)
+    assert torch.equal(d[-999:], moe.route_backward(r, tail, i2, w2, dw[:999].contiguous()))
+
+
 def test_empty_and_large_batches(moe):
     r = moe.Routing(2, "sigmoid")
     counts = torch.ones(8, dtype=torch.int32, device="cuda")
