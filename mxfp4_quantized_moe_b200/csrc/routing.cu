@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a) {
 // compare-exchange is two instructions.  Words are sorted in registers (Batcher's odd-even merge
 // sort of K2 at a time), and two descending lists merge by max(a_i, b_{K2-1-i}), the K2 largest
 // of both, which a bitonic half-cleaner sorts; three such merges across lanes leave the token's
-// K2 largest in all eight.  A token whose order the 23 bits (or fp32 keys) cannot decide, or that
+// K2 largest in all eight.  Where the 23 bits (or fp32 keys) cannot decide an order, sigmoid keys
+// of the chosen experts and at most one other are compared in fp64; a token that needs more, or
 // has fewer than k unmasked experts, goes through select() instead.
 template <int N>
 MOE_DEV void exchange(uint32_t (&v)[N], int i, int j) {  // the larger to i
@@ -399,7 +400,7 @@ MOE_DEV void join_two(float& m1, float& m2, float o1, float o2) {
 // G: groups when a group is NS / G whole slots and E = 8 NS (a folded reduction then gives lane q
 // the score of group q), 1 without groups, 0 for other groups of whole slots.  WHOLE: E = 8 NS.
 template <int NS, int K2, int G, bool WHOLE>
-__global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs a) {
   constexpr int NG = NS / 4;  // experts a lane holds in select()
   __shared__ double s_buf[4][32 * NG];
   __shared__ float s_bias[8 * NS];
@@ -599,11 +600,12 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
         scored ? (uint32_t)fminf((unit_margin + 0x1p-22f * (fabsf(hi) + range)) * per, 8388607.f) + 1u : 0u;
     const uint32_t below = __shfl_down_sync(kFull, mine, 1, 8);
     const float l1 = __shfl_down_sync(kFull, l, 1, 8), b1 = __shfl_down_sync(kFull, b, 1, 8);
-    unsure |= q + 1 < a.k && (mine >> 8) - (below >> 8) <= near && !(l == l1 && b == b1);
+    bool open = q + 1 < a.k && (mine >> 8) - (below >> 8) <= near && !(l == l1 && b == b1);
     const uint32_t reach = (last >> 8) > near ? ((last >> 8) - near) << 8 : 256u;
     bool close = false;
 #pragma unroll
     for (int i = 0; i < NS; ++i) close |= word[i] - reach < last - reach;  // reach <= word < last
+    int others = 0, other = 0;  // experts left out within reach of the last one chosen
     if (__any_sync(kFull, close)) {  // exact ties with the last one are in order
       const float lk = __shfl_sync(kFull, l, (lane & 24) | (a.k - 1));
       const float bk = __shfl_sync(kFull, b, (lane & 24) | (a.k - 1));
@@ -611,8 +613,45 @@ __global__ void __launch_bounds__(128) route4_kernel(RouteArgs a) {
       for (int i = 0; i < NS; ++i)
         if (word[i] - reach < last - reach) {
           const int o = 8 * i + q;
-          unsure |= !(fminf(__ldg(lg + o), FLT_MAX) == lk && (!a.bias || __ldg(a.bias + o) == bk));
+          if (!(fminf(__ldg(lg + o), FLT_MAX) == lk && (!a.bias || __ldg(a.bias + o) == bk))) {
+            ++others;
+            other = o;
+          }
         }
+    }
+    open |= others > 0;
+    if (!(scored && a.sigmoid)) {
+      unsure |= open;
+    } else if (__any_sync(kFull, open)) {
+      // one or no expert in question beside the chosen ones: all of them by their fp64 keys
+      const unsigned have = (__ballot_sync(kFull, others > 0) >> (lane & 24)) & 0xFFu;
+      others = (int)sum8((float)others);
+      unsure |= others > 1;
+      const int oe = __shfl_sync(kFull, other, (lane & 24) | (have ? __ffs(have) - 1 : 0));
+      auto key64 = [&](int i) {
+        const double s = 1.0 / (1.0 + exp(-(double)fminf(__ldg(lg + i), FLT_MAX)));
+        return a.bias ? s + (double)fminf(__ldg(a.bias + i), FLT_MAX) : s;
+      };
+      const double mykey = key64(e), okey = others ? key64(oe) : -1e300;
+      const bool before = others && (okey > mykey || (okey == mykey && oe < e));
+      int rank = before ? 1 : 0;  // this lane's place among the k chosen and the other one
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double k = __shfl_sync(kFull, mykey, (lane & 24) | j);
+        const int ke = __shfl_sync(kFull, e, (lane & 24) | j);
+        rank += j < a.k && j != q && (k > mykey || (k == mykey && ke < e)) ? 1 : 0;
+      }
+      const unsigned ahead = (__ballot_sync(kFull, slot && !before) >> (lane & 24)) & 0xFFu;
+      const int orank = others ? __popc(ahead) : 8;
+      int ne = orank == q ? oe : e;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = __shfl_sync(kFull, rank, (lane & 24) | j);
+        const int je = __shfl_sync(kFull, e, (lane & 24) | j);
+        ne = j < a.k && r == q ? je : ne;
+      }
+      e = slot ? ne : 0;
+      l = fminf(__ldg(lg + e), FLT_MAX);
     }
   }
   bool ok = true;
