@@ -1291,6 +1291,8 @@ __global__ void __launch_bounds__(NT, BLOCKS)
   for (int which = 0; which < 2; ++which) {
     float* part = partial_row(a, which);
     if (!part) continue;
+    // a caller's gradient is aligned to a feature; the partial sums are to vectors
+    const bool whole = (reinterpret_cast<uintptr_t>(part) & 15u) == 0;
     const Vals<V>* acc = which ? acc_b : acc_g;
     if (G > 1) {
 #pragma unroll
@@ -1313,7 +1315,11 @@ __global__ void __launch_bounds__(NT, BLOCKS)
       for (int c = 0; c < NC; ++c) {
         float f[V];
         get<V>(acc[c], f);
-        if (in[c]) {  // by single features: a caller's gradient is aligned to one
+        if (in[c] && whole) {
+          float4* to = reinterpret_cast<float4*>(part + h0 + 256 * c);
+          to[0] = make_float4(f[0], f[1], f[2], f[3]);
+          to[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else if (in[c]) {
 #pragma unroll
           for (int i = 0; i < V; ++i) part[h0 + 256 * c + i] = f[i];
         }
@@ -1475,7 +1481,7 @@ __global__ void __launch_bounds__(NT, BLOCKS)
 
 // d_weight (blockIdx.y 0) and d_bias (1) from the blocks' partial sums: 32 features per block,
 // its warps over the parts.
-constexpr int kReduceWarps = 16;  // most; fewer parts take fewer
+constexpr int kReduceWarps = 16, kPerWarp = (kParts + kReduceWarps - 1) / kReduceWarps;
 __global__ void __launch_bounds__(32 * kReduceWarps) norm_reduce_kernel(
     const float* __restrict__ partial, int parts, int H, float* __restrict__ d_weight,
     float* __restrict__ d_bias) {
@@ -1488,13 +1494,20 @@ __global__ void __launch_bounds__(32 * kReduceWarps) norm_reduce_kernel(
   wait_for_launcher();
   if (h < H) {
     const float* p = partial + (size_t)blockIdx.y * H + h;
-#pragma unroll 8
-    for (int i = warp; i < parts; i += blockDim.x >> 5) v += p[(size_t)i * 2 * H];
+    float each[kPerWarp];  // all requested before the first is added
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) {
+      const int part = warp + i * kReduceWarps;
+      each[i] = part < parts ? p[(size_t)part * 2 * H] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) v += each[i];
   }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && h < H) {
-    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v += s[i][lane];
+#pragma unroll
+    for (int i = 1; i < kReduceWarps; ++i) v += s[i][lane];
     out[h] = v;
   }
 }
@@ -1750,7 +1763,7 @@ cudaError_t launch_norm_backward(const NormGradArgs& a, int, cudaStream_t st) {
   if (parts == 1) return cudaSuccess;  // one block writes the gradients itself
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((a.H + 31) / 32, 2);
-  cfg.blockDim = dim3(parts >= 64 ? 32 * kReduceWarps : 256);
+  cfg.blockDim = dim3(32 * kReduceWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
