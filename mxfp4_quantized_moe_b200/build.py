@@ -5,8 +5,10 @@
   indices they read from the workspace and record MXFP4_MOE_ERR_DEVICE_BOUNDS instead of
   making the access (``mxfp4_moe_build_flags`` reports the build).  Loaded instead of the
   library when ``MXFP4_MOE_LIBRARY=debug``.
+* ``_edge.so``: the host side of the operators at the block's edge as a CPython module
+  (csrc/binding.cpp), which calls whichever of the two is loaded.
 
-Usage: ``python -m mxfp4_quantized_moe_b200.build [--verbose-ptxas]`` builds both.  Cross-compiles
+Usage: ``python -m mxfp4_quantized_moe_b200.build [--verbose-ptxas]`` builds all three.  Cross-compiles
 without a GPU.  The libraries statically link the CUDA runtime, so they load on a machine
 without a driver (calls then fail with MXFP4_MOE_ERR_CUDA).
 """
@@ -17,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -24,6 +27,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmxfp4_moe.so")
 LIB_DEBUG = os.path.join(HERE, "libmxfp4_moe_debug.so")
+BINDING_SOURCE = os.path.join("csrc", "binding.cpp")
+BINDING = os.path.join(HERE, "_edge.so")
 SOURCES = ["csrc/api.cu", "csrc/grouped_gemm.cu", "csrc/kernels_small.cu",
            "csrc/forward_static.cu", "csrc/selftest.cu", "csrc/residual_router.cu",
            "csrc/routing.cu", "csrc/norm.cu"]
@@ -46,6 +51,15 @@ def needs_build(lib: str = LIB) -> bool:
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:
+    """The library (or its debug build) and, beside it, the binding module."""
+    with ThreadPoolExecutor(max_workers=2) as pool:
+        beside = pool.submit(build_binding, force and not debug)
+        lib = build_library(force, ptxas_verbose, debug)
+        beside.result()
+    return lib
+
+
+def build_library(force: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
     if not force and not needs_build(lib):
         return lib
@@ -76,10 +90,39 @@ def build(force: bool = False, ptxas_verbose: bool = False, debug: bool = False)
     return lib
 
 
+def needs_binding() -> bool:
+    deps = (os.path.join(HERE, BINDING_SOURCE), os.path.join(ROOT, "include", "mxfp4_moe.h"))
+    return not os.path.exists(BINDING) or any(os.path.getmtime(d) > os.path.getmtime(BINDING)
+                                              for d in deps)
+
+
+def build_binding(force: bool = False) -> str:
+    """The host-side module `_edge` (C++ against torch's headers; no device code)."""
+    if not force and not needs_binding():
+        return BINDING
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-shared", "-fPIC",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in (os.path.join(at, "include"),
+                                os.path.join(at, "include", "torch", "csrc", "api", "include"),
+                                os.path.join(cuda, "include"), sysconfig.get_paths()["include"])),
+           "-o", BINDING + ".tmp", os.path.join(HERE, BINDING_SOURCE), "-L" + os.path.join(at, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, cwd=HERE, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the binding failed to compile:\n" + r.stdout + r.stderr)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build_all(force: bool = False, ptxas_verbose: bool = False) -> list[str]:
-    with ThreadPoolExecutor(max_workers=2) as pool:
-        both = [pool.submit(build, force, ptxas_verbose), pool.submit(build, force, False, True)]
-        return [b.result() for b in both]
+    with ThreadPoolExecutor(max_workers=3) as pool:
+        every = [pool.submit(build_library, force, ptxas_verbose),
+                 pool.submit(build_library, force, False, True),
+                 pool.submit(build_binding, force)]
+        return [b.result() for b in every]
 
 
 if __name__ == "__main__":

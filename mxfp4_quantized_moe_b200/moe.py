@@ -14,8 +14,12 @@ from typing import NamedTuple
 
 import torch
 
-from . import _lib
+from . import _edge, _lib
 from ._lib import Dims, Weights, check, lib
+
+_edge.bind(*(ctypes.cast(getattr(lib, "mxfp4_moe_" + name), ctypes.c_void_p).value for name in (
+    "route", "route_backward", "norm_forward", "norm_workspace_size", "norm_backward",
+    "checkpoint_pack", "checkpoint_unpack")))
 
 
 @dataclass
@@ -225,7 +229,9 @@ def grad_chain(g: torch.Tensor, dx: torch.Tensor | None, d_logits: torch.Tensor,
 # ---- the operators at the block's edge: routing, the norm, 8-bit checkpoints ----------------
 # These run on the device of their tensors (all on one), whichever device is current, on that
 # device's current stream or on `stream`; what they allocate belongs to that stream.  Rows and
-# vectors are dense; every output that a caller may pass is also what the call returns.
+# vectors are dense; every output that a caller may pass is also what the call returns.  The plain
+# call (outputs not given, the present stream and device) goes through _edge in one step; it
+# returns None for any other and for every error, and the long way below names it.
 _EMPTY = 256  # stands for the null pointer of a tensor without elements; never dereferenced
 _F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
 _ROWS = (torch.bfloat16, torch.float32)
@@ -257,7 +263,10 @@ def _tensor(t: torch.Tensor, name: str, shape, dtypes, index: int) -> int:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or _EMPTY
+    p = t.data_ptr()
+    if not p and t.numel():
+        raise ValueError(f"{name} has no memory")
+    return p or _EMPTY
 
 
 @dataclass
@@ -297,6 +306,11 @@ def route(routing: Routing, logits: torch.Tensor, bias: torch.Tensor | None = No
     balance bias fp32 [E] on the selection.  `counts` (int32 [E]) receives the slots of each
     expert.  Logits or biases of NaN, -inf or the lowest finite value mask an expert: it is
     selected last, with weight 0."""
+    if stream is None and topk_idx is None and topk_w is None and counts is None:
+        done = _edge.route(routing.k, routing.scores, routing.groups, routing.top_groups,
+                           routing.group_best, routing.renormalize, routing.scale, logits, bias)
+        if done is not None:
+            return done
     T, E = _logits_shape(logits)
     where = _elsewhere(logits, stream)
     if where is not None:
@@ -325,6 +339,12 @@ def route_backward(routing: Routing, logits: torch.Tensor, topk_idx: torch.Tenso
                    topk_w: torch.Tensor, d_topk_w: torch.Tensor,
                    d_logits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """d_logits fp32 [T, E] from d_topk_w fp32 [T, k], for what `route` returned on `logits`."""
+    if stream is None and d_logits is None:
+        done = _edge.route_backward(routing.k, routing.scores, routing.groups, routing.top_groups,
+                                    routing.group_best, routing.renormalize, routing.scale, logits,
+                                    topk_idx, topk_w, d_topk_w)
+        if done is not None:
+            return done
     T, E = _logits_shape(logits)
     where = _elsewhere(logits, stream)
     if where is not None:
@@ -418,6 +438,10 @@ def _format(dtype: torch.dtype) -> int:
 def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | None = None,
                     stream=None) -> Checkpoint:
     """Rows [T, H] (bf16 or fp32, H a multiple of 32) stored in 8 bits."""
+    if stream is None and out is None:
+        done = _edge.checkpoint_pack(x, format)
+        if done is not None:
+            return Checkpoint(*done, format)
     T, H, t = _rows_shape(x)
     where = _elsewhere(t, stream)
     if where is not None:
@@ -435,6 +459,11 @@ def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | Non
 def checkpoint_unpack(checkpoint: Checkpoint, dtype: torch.dtype = torch.bfloat16,
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The rows [T, H] that a checkpoint stands for, as bf16 or fp32."""
+    if stream is None and out is None and dtype in _ROWS:
+        done = _edge.checkpoint_unpack(checkpoint.codes, checkpoint.scales, checkpoint.format,
+                                       dtype == torch.float32)
+        if done is not None:
+            return done
     T, H, t = _rows_shape(checkpoint)
     where = _elsewhere(t, stream)
     if where is not None:
@@ -488,8 +517,19 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
     x: bf16 or fp32 rows, or a Checkpoint (normalised as the rows it stands for, into `dtype`,
     bf16 by default).  y: a residual; x_out = x + y, rounded to the rows' type, is returned and
     is what is normalised.  checkpoint: a format or a Checkpoint to fill with those rows."""
-    T, H, t = _rows_shape(x)
     stored = isinstance(x, Checkpoint)
+    if (stream is None and out is None and x_out is None and mean is None and rstd is None
+            and not isinstance(checkpoint, Checkpoint)):
+        done = None
+        if not stored and dtype in (None, x.dtype):
+            done = _edge.norm_forward(x, None, None, False, y, weight, bias, kind, eps, checkpoint)
+        elif stored and y is None and checkpoint is None and dtype in (None, *_ROWS):
+            done = _edge.norm_forward(x.codes, x.scales, x.format, dtype == torch.float32, None,
+                                      weight, bias, kind, eps, None)
+        if done is not None:
+            kept = None if checkpoint is None else Checkpoint(done[4], done[5], checkpoint)
+            return NormOut(*done[:4], kept)
+    T, H, t = _rows_shape(x)
     if stored:
         if y is not None or checkpoint is not None:
             raise ValueError("a checkpoint as input takes no residual and fills no checkpoint")
@@ -566,6 +606,13 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     be g itself).  params=False computes dx alone and returns None for the other two; d_bias is
     None for "rms" unless a tensor is given.  ws: scratch of norm_workspace_bytes (else
     allocated); two captured graphs that may run at once need one each."""
+    if (stream is None and params and dx is None and d_weight is None and d_bias is None
+            and ws is None):
+        done = (_edge.norm_backward(d_out, x.codes, x.scales, x.format, mean, rstd, weight, kind, g)
+                if isinstance(x, Checkpoint) else
+                _edge.norm_backward(d_out, x, None, None, mean, rstd, weight, kind, g))
+        if done is not None:
+            return done
     T, H, t = _rows_shape(x)
     dtype = d_out.dtype
     dims = _norm_dims(T, H, kind, 0.0, dtype, dtype if weight is None else weight.dtype)

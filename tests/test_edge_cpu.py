@@ -199,3 +199,24 @@ def test_grad_chain_without_dx(L, reached):
     gc = L.lib.mxfp4_moe_grad_chain
     assert gc(4, 64, 8, A, None, B, C, D, None) in reached
     assert gc(4, 64, 8, A, ODD, B, C, D, None) == L.ERR_INVALID_ARG
+
+
+def test_the_one_step_binding_leaves_other_calls_to_the_wrappers():
+    """_edge answers None, with no error set, for whatever is not a plain call."""
+    from mxfp4_quantized_moe_b200 import moe
+    e = moe._edge
+    x, l = torch.zeros(3, 64), torch.zeros(3, 8)
+    how = (2, "softmax", 1, 1, 1, True, 1.0)
+    idx = torch.zeros(3, 2, dtype=torch.int32)
+    for call in (lambda: e.route(*how, l, None), lambda: e.route(*how, None, None),
+                 lambda: e.route("two", *how[1:], l, None), lambda: e.route(*how, 7, "b"),
+                 lambda: e.route(2, "relu", *how[2:], l, None),
+                 lambda: e.route_backward(*how, l, idx, torch.zeros(3, 2), torch.zeros(3, 2)),
+                 lambda: e.norm_forward(x, None, None, False, None, None, None, "layer", 1e-5, None),
+                 lambda: e.norm_forward(x, x, "e4m3", False, None, None, None, "rms", "eps", None),
+                 lambda: e.norm_backward(x, x, None, None, None, x, None, "rms", None),
+                 lambda: e.checkpoint_pack(x, "e4m3"), lambda: e.checkpoint_pack(x, 3),
+                 lambda: e.checkpoint_unpack(x, None, "e4m3", False)):
+        assert call() is None
+    with pytest.raises(TypeError):
+        e.route(l)
