@@ -82,6 +82,11 @@ float real(PyObject* o) {
   if (v == -1.0 && PyErr_Occurred()) throw Other{};
   return (float)v;
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Other{};
+  return v != 0;
+}
 int named(PyObject* o, const char* zero, const char* one) {
   if (!PyUnicode_Check(o)) throw Other{};
   if (PyUnicode_CompareWithASCIIString(o, zero) == 0) return 0;
@@ -118,7 +123,7 @@ PyObject* plain(Py_ssize_t n, Py_ssize_t want, const F& f) {
 // k, scores, groups, top_groups, group_best, renormalize, scale
 mxfp4_moe_routing routing_of(PyObject* const* a, const at::Tensor& logits) {
   return {(int32_t)logits.size(0), (int32_t)logits.size(1), number(a[0]), scores_of(a[1]),
-          number(a[2]), number(a[3]), number(a[4]), PyObject_IsTrue(a[5]) == 1, real(a[6])};
+          number(a[2]), number(a[3]), number(a[4]), truth(a[5]), real(a[6])};
 }
 
 // (routing x 7, logits, bias) -> (topk_idx, topk_w)
@@ -190,7 +195,7 @@ const void* vector_of(PyObject* o, int H, int dev, int* format, bool first) {
 PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return plain(n, 10, [&]() -> PyObject* {
     const Rows r(a[0], a[1], a[2]);
-    const at::ScalarType type = r.x ? r.t->scalar_type() : PyObject_IsTrue(a[3]) == 1 ? at::kFloat : at::kBFloat16;
+    const at::ScalarType type = r.x ? r.t->scalar_type() : truth(a[3]) ? at::kFloat : at::kBFloat16;
     mxfp4_moe_norm d{r.T, r.H, kind_of(a[7]), real(a[8]), rows_format_of(type), 0};
     const void* weight = vector_of(a[5], r.H, r.dev, &d.param_format, true);
     const void* bias = vector_of(a[6], r.H, r.dev, &d.param_format, weight == nullptr);
@@ -263,7 +268,7 @@ PyObject* checkpoint_unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return plain(n, 4, [&]() -> PyObject* {
     if (!given(a[1])) throw Other{};
     const Rows r(a[0], a[1], a[2]);
-    const bool f32 = PyObject_IsTrue(a[3]) == 1;
+    const bool f32 = truth(a[3]);
     const at::Tensor out = fresh({r.T, r.H}, f32 ? at::kFloat : at::kBFloat16, r.dev);
     done(entry.checkpoint_unpack(r.T, r.H, f32 ? MXFP4_MOE_ROWS_FP32 : MXFP4_MOE_ROWS_BF16, &r.from,
                                  out.data_ptr(), stream_of(r.dev)));

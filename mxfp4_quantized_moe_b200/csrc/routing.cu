@@ -422,8 +422,17 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
 #pragma unroll
   for (int i = 0; i < NS; ++i) x[i] = WHOLE || 8 * i + q < a.E ? __ldg(lg + 8 * i + q) : -FLT_MAX;
   if (scored) {
-    for (int e = threadIdx.x; e < 8 * NS; e += blockDim.x)
-      s_bias[e] = a.bias && e < a.E ? fminf(fmaxf(__ldg(a.bias + e), -FLT_MAX), FLT_MAX) : 0.f;
+    float b[NS / 4];  // all requested before the first is stored (one warp alone takes them all)
+#pragma unroll
+    for (int i = 0; i < NS / 4; ++i) {
+      const int e = threadIdx.x + i * blockDim.x;
+      b[i] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NS / 4; ++i) {
+      const int e = threadIdx.x + i * blockDim.x;
+      if (e < 8 * NS) s_bias[e] = fminf(fmaxf(b[i], -FLT_MAX), FLT_MAX);
+    }
     __syncthreads();
   }
   if (row0 >= a.T) return;  // warp-uniform
