@@ -296,7 +296,8 @@ MXFP4_MOE_API int mxfp4_moe_grad_chain(int32_t T, int32_t H, int32_t E, const ui
  *             weights come from s.  Order is decided on fp64 keys: fp32 keys are used where
  *             their error cannot change it, and the row is redone in fp64 where it could.
  *     groups > 1: experts [g E/groups, (g+1) E/groups) form group g; its score is the sum of
- *             its group_best largest keys (s_e without a bias; masked experts are left out),
+ *             its group_best largest keys (s_e without a bias, or with group_best 1 the largest
+ *             l_e, which orders alike and does not saturate; masked experts are left out),
  *             and only the top_groups best groups stay eligible (ties to the lower group)
  *     idx   = the k largest keys among the eligible experts, largest first, ties to the lower
  *             index.  Masked experts of the kept groups fill up in index order when fewer

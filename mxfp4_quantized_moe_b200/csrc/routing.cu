@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
     const bool real = q < a.groups, kept = real && rank < a.top_groups;
     if (scored) {
       const float in = min8(kept ? mine : INFINITY), no = max8(real && !kept ? mine : -FLT_MAX);
-      unsure = no > -FLT_MAX && !(in - no > 2.f * unit_margin + 0x1p-21f * fabsf(in));
+      unsure |= no > -FLT_MAX && !(in - no > 2.f * unit_margin + 0x1p-21f * fabsf(in));
     }
     const uint32_t keep = __ballot_sync(kFull, kept) >> (lane & 24);
     if constexpr (G > 1) {
@@ -603,7 +603,6 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
   }
   const bool slot = q < a.k;
   int e = slot ? 255 - (int)(mine & 255u) : 0;
-  unsure |= last < (2u << 8);  // an expert out of the choice
   e = e < a.E ? e : 0;
   float l = fminf(__ldg(lg + e), FLT_MAX);
   const float b = a.bias ? __ldg(a.bias + e) : 0.f;
@@ -614,11 +613,16 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
     const uint32_t below = __shfl_down_sync(kFull, mine, 1, 8);
     const float l1 = __shfl_down_sync(kFull, l, 1, 8), b1 = __shfl_down_sync(kFull, b, 1, 8);
     bool open = q + 1 < a.k && (mine >> 8) - (below >> 8) <= near && !(l == l1 && b == b1);
-    const uint32_t reach = (last >> 8) > near ? ((last >> 8) - near) << 8 : 256u;
+    // With place 1 chosen or within reach (masked, missing, too far below) select() decides;
+    // else what is within reach has a place, and so a logit
+    const bool floor_near = (last >> 8) <= near + 1u;
+    unsure |= floor_near;
+    const uint32_t reach = floor_near ? last : ((last >> 8) - near) << 8;
     bool close = false;
 #pragma unroll
     for (int i = 0; i < NS; ++i) close |= word[i] - reach < last - reach;  // reach <= word < last
     int others = 0, other = 0;  // experts left out within reach of the last one chosen
+    bool tied = false;          // one of them equals the last one chosen
     if (__any_sync(kFull, close)) {  // exact ties with the last one are in order
       const float lk = __shfl_sync(kFull, l, (lane & 24) | (a.k - 1));
       const float bk = __shfl_sync(kFull, b, (lane & 24) | (a.k - 1));
@@ -629,6 +633,8 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
           if (!(fminf(__ldg(lg + o), FLT_MAX) == lk && (!a.bias || __ldg(a.bias + o) == bk))) {
             ++others;
             other = o;
+          } else {
+            tied = true;
           }
         }
     }
@@ -636,14 +642,18 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
     if (!(scored && a.sigmoid)) {
       unsure |= open;
     } else if (__any_sync(kFull, open)) {
-      // one or no expert in question beside the chosen ones: all of them by their fp64 keys
+      // one or no expert in question beside the chosen ones: all of them by their fp64 keys (an
+      // equal of the last one, left out, goes ahead of whatever that one turns out to pass)
+      const unsigned opens = (__ballot_sync(kFull, open) >> (lane & 24)) & 0xFFu;
+      unsure |= tied && opens != 0u;
       const unsigned have = (__ballot_sync(kFull, others > 0) >> (lane & 24)) & 0xFFu;
       others = (int)sum8((float)others);
       unsure |= others > 1;
       const int oe = __shfl_sync(kFull, other, (lane & 24) | (have ? __ffs(have) - 1 : 0));
       auto key64 = [&](int i) {
-        const double s = 1.0 / (1.0 + exp(-(double)fminf(__ldg(lg + i), FLT_MAX)));
-        return a.bias ? s + (double)fminf(__ldg(a.bias + i), FLT_MAX) : s;
+        const double v = (double)fminf(__ldg(lg + i), FLT_MAX);
+        if (!a.bias) return v;  // scores order like logits, which do not saturate
+        return 1.0 / (1.0 + exp(-v)) + (double)fminf(__ldg(a.bias + i), FLT_MAX);
       };
       const double mykey = key64(e), okey = others ? key64(oe) : -1e300;
       const bool before = others && (okey > mykey || (okey == mykey && oe < e));
@@ -679,6 +689,8 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
       if (scored) select<double, NG, 1>(a, tk, s_buf[warp], p);
       else select<float, NG, 1>(a, tk, reinterpret_cast<float*>(s_buf[warp]), p);
       __syncwarp();
+      float ttop = 0.f, ttotal = 1.f;  // infinite logits clamped
+      if (!a.sigmoid && !a.renorm) softmax_stats<float, NG>(tk, ttop, ttotal);
       const int pe = __shfl_sync(kFull, p.e[0], q);
       const float pl = __shfl_sync(kFull, p.l[0], q);
       const bool po = __shfl_sync(kFull, (int)p.ok[0], q);
@@ -686,6 +698,8 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
         e = pe;
         l = pl;
         ok = po;
+        top = ttop;
+        total = ttotal;
       }
     }
   }
@@ -771,7 +785,7 @@ __global__ void __launch_bounds__(128) route4_backward_kernel(RouteArgs a, const
   for (int i = 0; i < NV; ++i) mine[8 * i + q] = row_v[i];
   // two slots that name one expert see it in its tag; they are added one after another
   if (put) s_tag[warp][tok][e] = (uint8_t)q;
-  float d = w * (dw - (a.renorm ? dot * a.inv_scale : 0.f));
+  float d = w != 0.f ? w * (dw - (a.renorm ? dot * a.inv_scale : 0.f)) : 0.f;
   if (a.sigmoid) d /= 1.f + expf(le);  // times 1 - sigmoid(l)
   __syncwarp();
   if (!__any_sync(kFull, put && s_tag[warp][tok][e] != q)) {

@@ -56,7 +56,8 @@ def route(logits, k, bias=None, scores="softmax", groups=1, top_groups=1, group_
             key = np.minimum(np.where(gone, 0.0, logits[t]), -LOWEST)
         eligible = np.ones(E, dtype=bool)
         if groups > 1:
-            by = key if bias is not None else s
+            # the largest score is the largest logit's, which fp64 scores may no longer tell
+            by = key if bias is not None or group_best == 1 else s
             total = []
             for g in range(groups):
                 mine = sorted((by[e] for e in range(g * size, (g + 1) * size) if not gone[e]),

@@ -293,3 +293,86 @@ def test_other_stream_and_captured_replay(moe):
     g.replay()
     i4, w4 = moe.route(r, static, bias)
     assert torch.equal(i3, i4) and torch.equal(w3, w4)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,k", [(4, 1, 2), (32, 4, 4), (40, 1, 8), (128, 8, 6), (64, 1, 12)])
+def test_infinite_logits_without_renormalisation(moe, scores, E, groups, k):
+    """+inf is the largest finite value: the softmax of a row that holds some is shared by them."""
+    logits = normal(9, E, E)
+    inf = float("inf")
+    logits[0, 0] = logits[1, 1] = logits[1, E - 1] = logits[3, 2] = inf
+    logits[2] = inf
+    logits[4, 0], logits[4, 1:] = inf, -inf
+    logits[5, 0], logits[5, 1] = 3e38, inf
+    for best in (1, 2):
+        r = moe.Routing(k, scores, groups, max(1, groups // 2), best if groups > 1 else 1, False, 2.5)
+        for bias in (None, torch.zeros(E)):
+            idx, w = moe.route(r, logits.cuda(), None if bias is None else bias.cuda())
+            ri, rw = O.route(logits.double().numpy(), k, None if bias is None else bias.numpy(),
+                             **oracle_args(r))
+            assert np.array_equal(idx.cpu().numpy(), ri)
+            # scores of ordinary rows as in check(); those of the infinite ones are 1, 1/n or 0
+            np.testing.assert_allclose(w.double().cpu().numpy(), rw, rtol=weight_bound(logits.double().numpy()),
+                                       atol=1e-37)
+            d = moe.route_backward(r, logits.cuda(), idx, w, torch.ones(9, k, device="cuda"))
+            assert torch.isfinite(d).all()
+
+
+def test_exact_tie_beside_a_near_one(moe):
+    """The last place is held by one of two equal experts, and the place before it by one whose key
+    is off by less than fp32 tells: where the equal ones rank first, both are chosen."""
+    T, E = 256, 32
+    gen = torch.Generator().manual_seed(21)
+    la = torch.rand(T, generator=gen) * 2 - 1
+    key = torch.sigmoid(la.double()) + torch.tensor(0.05).double()
+    lx = torch.log(key / (1 - key)).float()  # its key is the others' up to the rounding of lx
+    logits = torch.full((T, E), -10.0) + normal(T, E, 22, 0.5)
+    bias = torch.zeros(E)
+    for x, a, b, k in ((1, 5, 6, 2), (9, 2, 30, 2), (31, 8, 24, 2)):
+        rows, shift = logits.clone(), bias.clone()
+        rows[:, x], rows[:, a], rows[:, b] = lx, la, la
+        shift[a] = shift[b] = 0.05
+        kx = torch.sigmoid(lx.double())
+        first = kx < key
+        assert 32 < int(first.sum()) < T - 32  # both orders
+        for groups in (1, 4):
+            check(moe, moe.Routing(k, "sigmoid", groups, groups), rows, shift)
+            check(moe, moe.Routing(k, "sigmoid", groups, groups, renormalize=False), rows, shift)
+
+
+def test_zero_weight_with_an_infinite_gradient(moe):
+    """A slot of weight 0 has no gradient, whatever the other slots hold."""
+    logits = normal(2, 16, 3)
+    logits[:, 2:] = float("-inf")
+    for k in (4, 12):
+        for scores in ("softmax", "sigmoid"):
+            r = moe.Routing(k, scores)
+            idx, w = moe.route(r, logits.cuda())
+            assert (w[:, 2:] == 0).all()
+            dw = torch.ones(2, k, device="cuda")
+            dw[1, 0] = float("inf")
+            d = moe.route_backward(r, logits.cuda(), idx, w, dw)
+            assert torch.isfinite(d[0]).all() and (d[:, 2:] == 0).all()
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,best", [(1, 1), (4, 1), (4, 2)])
+def test_saturated_scores_order_like_their_logits(moe, scores, groups, best):
+    """Logits of which fp64 scores no longer tell the order (sigmoid(40) = sigmoid(50) = 1)."""
+    for E, k in ((32, 4), (64, 8), (64, 12)):
+        logits = torch.cat([normal(24, E, E, 4.0) + 60, normal(24, E, E + 1, 60.0)])
+        check(moe, moe.Routing(k, scores, groups, max(1, groups // 2), best), logits, None)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(9, 8), (9, 4), (40, 8), (200, 6), (61, 12)])
+def test_biases_far_above_the_scores(moe, scores, E, k):
+    """Keys whose fp32 step is as wide as the scores: the order is that of the fp64 keys, and a
+    masked expert beside the last one chosen stays out."""
+    logits = normal(40, E, E)
+    for t in range(0, 40, 2):
+        logits[t, (3 * t) % E] = float("nan") if t % 4 else float("-inf")
+    for level, spread in ((1e5, 5.0), (1e5, 0.0), (3e7, 0.0), (-2e4, 20.0)):
+        bias = level + normal(1, E, 31)[0] * spread
+        check(moe, moe.Routing(k, scores, renormalize=False), logits, bias)
