@@ -84,9 +84,18 @@ MOE_DEV double exp_of(double x) { return exp(x); }
 // Bounds on what the fp32 keys may be off.  A sigmoid or softmax score in [0, 1] is within
 // 2^-20 of its value (expf 2 ulp, at most eight sums in sequence, a division, and the rounding
 // of the exponent, |x| e^x 2^-24 <= 2^-25), and adding the bias rounds by 2^-24 of the key.
-// Two keys further apart than twice that are in order; these are twice that again.
+// Two keys further apart than twice that are in order; this is twice that again.
 MOE_DEV float key_margin(float key) { return 0x1p-18f + 0x1p-22f * fabsf(key); }
-MOE_DEV float group_margin(float score) { return 0x1p-17f + 0x1p-21f * fabsf(score); }
+// A group's score is the sum of its keys m1 and m2 (m2 = 0: m1 alone).  Key i is off by what its
+// score is, and rounds by 2^-24 |m_i|; the largest and the second largest of several keys are off by
+// no more than that, since value + bound and value - bound rise with the value; and the sum rounds
+// by 2^-24 (|m1| + |m2|).  In all `scores`, what two scores may be off together, and
+// 2^-23 (|m1| + |m2|): relative to the keys, not to a sum in which they may cancel.  Twice the
+// latter, for the rounding of score - slack and score + slack as well; each product by itself, so
+// that keys near the largest value do not overflow.
+MOE_DEV float group_slack(float m1, float m2, float scores) {
+  return scores + (0x1p-22f * fabsf(m1) + 0x1p-22f * fabsf(m2));
+}
 
 // One token's logits over the lanes of a warp: lane l holds experts l NG .. l NG + NG - 1.
 template <int NG>
@@ -199,7 +208,8 @@ MOE_DEV bool select(const RouteArgs& a, const Token<NG>& t, F* buf, Picked<NS>& 
       }
     }
     __syncwarp();
-    const F score = m1 + ((a.best2 && m2 > (F)-INFINITY) ? m2 : (F)0);
+    if (!(a.best2 && m2 > (F)-INFINITY)) m2 = 0;
+    const F score = m1 + m2;
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
       const F o = __shfl_sync(kFull, score, g);
@@ -208,11 +218,14 @@ MOE_DEV bool select(const RouteArgs& a, const Token<NG>& t, F* buf, Picked<NS>& 
     const bool mine = lane < a.groups;
     const unsigned kept = __ballot_sync(kFull, mine && rank < a.top_groups);
     if (fast && (approx || a.best2) && a.top_groups < a.groups) {
-      const unsigned in = __ballot_sync(kFull, mine && rank == a.top_groups - 1);
-      const unsigned out = __ballot_sync(kFull, mine && rank == a.top_groups);
-      const F si = __shfl_sync(kFull, score, __ffs(in) - 1);
-      const F so = __shfl_sync(kFull, score, __ffs(out) - 1);
-      if (so > (F)-INFINITY && !(si - so > (F)group_margin((float)si))) return false;
+      // every kept group must lie above every other one (those without experts, at -inf, do not
+      // count) by what both may be off
+      const bool some = mine && score > (F)-INFINITY;
+      const float slack = some ? group_slack((float)m1, (float)m2, 0x1p-18f) : 0.f;
+      const float low = mine && rank < a.top_groups ? (float)score - slack : INFINITY;
+      const float high = some && rank >= a.top_groups ? (float)score + slack : -INFINITY;
+      const float out = warp_maxf(high);
+      if (out > -INFINITY && !(-warp_maxf(-low) > out)) return false;
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
@@ -452,7 +465,9 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
   }
   // Scores as keys.  ex2.approx and rcp.approx are within 2 ulp and 1 ulp, the exponent's
   // rounding moves e^-l by |l| 2^-24: a sigmoid is within 4.3 2^-24 of its value.  A softmax score
-  // is within 2^-22 plus what its sum is off, less than 2^-19 of the score: see `margin`.
+  // is within 2^-22, plus what the sum of exps is off: at most 38 2^-24 of the score (31 + 3 sums,
+  // expf), in the same direction for all scores of the token.  `unit_margin` bounds what two scores
+  // may be off against one another, its double what two sums of two scores may.
   const float inv_total = 1.f / total;
   auto score = [&](float l) {
     if (!a.sigmoid) return exp2_approx((l - top) * kLog2e) * inv_total;
@@ -469,7 +484,13 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
   const float unit_margin = 0x1p-20f + (a.sigmoid ? 0.f : 0x1p-18f * inv_total);
   bool unsure = !(top < INFINITY);
   if constexpr (G != 1) {
-    float mine = -FLT_MAX;  // lane q: score of group q
+    float mine = -FLT_MAX;  // lane q: score of group q, and how far it may be off
+    float slack = 0.f;
+    auto total_of = [&](float m1, float m2) {
+      if (!(a.best2 && m2 > -FLT_MAX)) m2 = 0.f;
+      mine = m1 + m2;
+      slack = m1 > -FLT_MAX ? group_slack(m1, m2, unit_margin) : 0.f;
+    };
     int span = 0;
     float v1[G ? G : 1], v2[G ? G : 1];
     if constexpr (G > 1) {
@@ -504,8 +525,11 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
       }
       // lane q holds group q / (8 / G)
       const int from = (lane & 24) | (q * (8 / G) & 7);
-      mine = v1[0] + (a.best2 && v2[0] > -FLT_MAX ? v2[0] : 0.f);
-      mine = __shfl_sync(kFull, mine, from);
+      total_of(v1[0], v2[0]);
+      if constexpr (G < 8) {
+        mine = __shfl_sync(kFull, mine, from);
+        slack = __shfl_sync(kFull, slack, from);
+      }
     } else {
       span = a.gsize >> 3;  // slots of a group
       float m1 = -FLT_MAX, m2 = -FLT_MAX;
@@ -520,7 +544,7 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
 #pragma unroll
             for (int o = 1; o < 8; o *= 2)
               join_two(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
-            if (q == g) mine = m1 + (a.best2 && m2 > -FLT_MAX ? m2 : 0.f);
+            if (q == g) total_of(m1, m2);
             ++g;
             left = span;
             m1 = m2 = -FLT_MAX;
@@ -537,8 +561,9 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
     }
     const bool real = q < a.groups, kept = real && rank < a.top_groups;
     if (scored) {
-      const float in = min8(kept ? mine : INFINITY), no = max8(real && !kept ? mine : -FLT_MAX);
-      unsure |= no > -FLT_MAX && !(in - no > 2.f * unit_margin + 0x1p-21f * fabsf(in));
+      const float in = min8(kept ? mine - slack : INFINITY);
+      const float no = max8(real && !kept && mine > -FLT_MAX ? mine + slack : -INFINITY);
+      unsure |= no > -INFINITY && !(in > no);
     }
     const uint32_t keep = __ballot_sync(kFull, kept) >> (lane & 24);
     if constexpr (G > 1) {
