@@ -1082,12 +1082,16 @@ __global__ void __launch_bounds__(NT, BLOCKS)
         constexpr int c = decltype(cc)::value;
         constexpr int tx = (j * NC + c) * kStage<SRC>, td = (j * NC + c) * kStage<kGrad>;
         const uint32_t n = in[c] && live ? 16u : 0u;
+        // Features past the row's end have d_out = 0, and for x the row's own (the lane's first
+        // vector, or the row's): with x = 0 there x_hat = -mean rstd need not be a finite number.
+        const uint8_t* xc = c == 0 || in[c] ? x : x - 256 * c * kX;
+        const uint32_t nx = live ? 16u : 0u;
         if constexpr (kRows) {
-          copy_async16<tx, 256 * c * kX, SRC == kF32>(stage_x, x, n);
-          if constexpr (SRC == kF32) copy_async16<tx + 512, 256 * c * kX + 16, SRC == kF32>(stage_x, x, n);
+          copy_async16<tx, 256 * c * kX, SRC == kF32>(stage_x, xc, nx);
+          if constexpr (SRC == kF32) copy_async16<tx + 512, 256 * c * kX + 16, SRC == kF32>(stage_x, xc, nx);
         } else {
-          copy_async8<tx, 256 * c>(stage_x, x, n / 2);
-          byte[j][c] = __ldg(a.from.scales + at / 32 + (in[c] ? h0 / 32 + 8 * c : 0));
+          copy_async8<tx, 256 * c>(stage_x, xc, nx / 2);
+          byte[j][c] = __ldg(a.from.scales + at / 32 + h0r / 32 + (c == 0 || in[c] ? 8 * c : 0));
         }
         copy_async16<td, 256 * c * kD, F32>(stage_d, d, n);
         if constexpr (F32) copy_async16<td + 512, 256 * c * kD + 16, F32>(stage_d, d, n);

@@ -2,9 +2,11 @@
 and that ordinary batches do not reach, against the fp64 oracle or the entry points themselves.
 """
 
+import numpy as np
 import pytest
 import torch
 
+from test_gpu_norm import R, TYPES, f64, rows
 from test_gpu_routing import check, normal
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +76,36 @@ def test_group_sums_beside_the_largest_values(moe, E, groups, k):
     for n in (1, 2, 3):
         r = moe.Routing(k, "sigmoid", groups, n, 2, renormalize=False)
         check(moe, r, logits, bias.reshape(E))
+
+
+# ---- the norm's gradients of rows far from zero ---------------------------------------------
+@pytest.mark.parametrize("H", [64, 512, 4384])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value,eps", [(2.0 ** 114, 1e-12), (2.0 ** 114, 1e-5), (-2.0 ** 100, 1e-20)])
+def test_gradient_of_constant_rows_of_large_values(moe, H, dtype, value, eps):
+    """A constant row has x_hat = 0 whatever its mean: dx = rstd (v - mean v).  Lanes past the
+    row's end hold no features, and mean * rstd, which may be beyond fp32, is no part of it."""
+    dt = TYPES[dtype]
+    mean = torch.full((3,), value, device="cuda")
+    rstd = torch.full((3,), eps ** -0.5, device="cuda")
+    d, g = rows(3, H, dt, 1).cuda(), rows(3, H, dt, 2).cuda()
+    v, r = f64(d), f64(rstd)[:, None]
+    for off in (0, 1, None):  # in place, without vector alignment, from a checkpoint
+        x = torch.full((3 * H + 8,), value, dtype=dt, device="cuda")[off or 0:][:3 * H].view(3, H)
+        if off is None:
+            x = moe.checkpoint_pack(x)
+        if H & (H - 1) == 0:  # the mean is exact
+            f = moe.norm_forward(x, eps=eps, dtype=dt)
+            assert not f.out.any() and torch.equal(f.mean, mean)
+        for grad in (None, g):
+            dx, dw, db = moe.norm_backward(d, x, mean, rstd, g=grad)
+            ref = (v - v.mean(1, keepdims=True)) * r
+            mag = (np.abs(v) + np.abs(v).mean(1, keepdims=True)) * r
+            if grad is not None:
+                ref, mag = ref + f64(grad), mag + np.abs(f64(grad))
+            # the mean's sum and product, the two products and the sum with g
+            tol = 80 * R * mag
+            tol = tol + torch.finfo(dt).eps / 2 * (np.abs(ref) + tol)
+            assert np.all(np.abs(f64(dx) - ref) <= tol)
+            assert not dw.any()
+            assert np.all(np.abs(f64(db) - v.sum(0)) <= 4 * R * np.abs(v).sum(0))
