@@ -1483,18 +1483,26 @@ bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // 60 us in the persistent one.
 constexpr int kManyRows = 600;
 
-template <class K>
-cudaError_t allow_shared(K kern, int bytes) {  // static shared memory included: 48 KB need no leave
-  if (bytes <= 32 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// Leave for a launch of `bytes` of dynamic shared memory.  The leave belongs to the kernel, not to
+// the launch, and other host threads launch it for rows of other lengths: so every call asks for
+// the same, the most that any H of this kernel takes.
+template <int MOST, class K>
+cudaError_t allow_shared(K kern, int bytes) {
+  if (bytes > MOST) return cudaErrorInvalidValue;
+  if (MOST <= 32 * 1024) return cudaSuccess;  // static shared memory included: 48 KB need no leave
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
 }
+// Bytes of the unaligned rows that the warps of a block (NT / 32, NC vectors of 8 features a lane)
+// hold at a time, at most: fewer groups of more warps pad less.
+template <int NC, int E, int NT> constexpr int kLoosePlaces = NT / 32 * (16 + 256 * NC * E);
 
 template <int SRC, bool F32, bool RES, int NC, int RB, int NT, int BLOCKS>
 cudaError_t forward_persistent(const NormArgs& a, int W, int sms, cudaStream_t st) {
   auto kern = norm_forward_many_kernel<SRC, F32, RES, NC, RB, NT, BLOCKS>;
   const int groups = NT / (32 * W);
-  const int smem = W * groups * RB * NC * kStage<SRC> * (RES ? 2 : 1);  // at most 128 KB
-  const cudaError_t e = allow_shared(kern, smem);
+  constexpr int kWarpBytes = RB * NC * kStage<SRC> * (RES ? 2 : 1);
+  const int smem = W * groups * kWarpBytes;  // at most 128 KB
+  const cudaError_t e = allow_shared<NT / 32 * kWarpBytes>(kern, smem);
   if (e != cudaSuccess) return e;
   const long long need = ((long long)a.T + RB * groups - 1) / (RB * groups);
   const long long most = (long long)sms * BLOCKS;
@@ -1505,8 +1513,9 @@ template <bool F32, bool RES, int NC, int RB, int NT, int BLOCKS>
 cudaError_t forward_loose(const NormArgs& a, int W, int sms, cudaStream_t st) {
   auto kern = norm_forward_loose_kernel<F32 ? kF32 : kBf16, F32, RES, NC, RB, NT, BLOCKS>;
   const int groups = NT / (32 * W);
-  const int smem = groups * 2 * RB * (RES ? 2 : 1) * (int)LooseRow<F32 ? 4 : 2>::place(a.H);
-  const cudaError_t e = allow_shared(kern, smem);
+  constexpr int E = F32 ? 4 : 2, kRowsHeld = 2 * RB * (RES ? 2 : 1);
+  const int smem = groups * kRowsHeld * (int)LooseRow<E>::place(a.H);
+  const cudaError_t e = allow_shared<kRowsHeld * kLoosePlaces<NC, E, NT>>(kern, smem);
   if (e != cudaSuccess) return e;
   const long long need = ((long long)a.T + RB * groups - 1) / (RB * groups);
   const long long most = (long long)sms * BLOCKS;
@@ -1587,10 +1596,11 @@ cudaError_t backward_staged(const NormGradArgs& a, int W, int* parts, cudaStream
   auto kern = norm_backward_staged_kernel<SRC, F32, HASG, NC, R, NT, BLOCKS>;
   constexpr int kGrad = F32 ? kF32 : kBf16;
   const int groups = NT / (32 * W);
-  int smem = W * groups * R * NC * (kStage<SRC> + kStage<kGrad> * (HASG ? 2 : 1));
-  const int sums = 4 * 256 * NC * W * groups;  // the groups' sums at the end
-  if (smem < sums) smem = sums;
-  const cudaError_t e = allow_shared(kern, smem);
+  constexpr int kTurns = R * NC * (kStage<SRC> + kStage<kGrad> * (HASG ? 2 : 1));
+  constexpr int kSums = 4 * 256 * NC;  // the groups' sums at the end
+  constexpr int kWarpBytes = kTurns > kSums ? kTurns : kSums;
+  const int smem = W * groups * kWarpBytes;
+  const cudaError_t e = allow_shared<NT / 32 * kWarpBytes>(kern, smem);
   if (e != cudaSuccess) return e;
   const Share sh = share_rows(a.T, R * groups, BLOCKS);
   *parts = sh.blocks;
@@ -1602,10 +1612,10 @@ template <bool F32, bool HASG, int NC, int R, int NT, int BLOCKS>
 cudaError_t backward_loose(const NormGradArgs& a, int W, int* parts, cudaStream_t st) {
   auto kern = norm_backward_loose_kernel<F32, HASG, NC, R, NT, BLOCKS>;
   const int groups = NT / (32 * W);
-  int smem = groups * 2 * R * (HASG ? 3 : 2) * (int)LooseRow<F32 ? 4 : 2>::place(a.H);
-  const int sums = 4 * a.H * groups;  // the groups' sums at the end
-  if (smem < sums) smem = sums;
-  const cudaError_t e = allow_shared(kern, smem);
+  constexpr int E = F32 ? 4 : 2, kRowsHeld = 2 * R * (HASG ? 3 : 2);
+  static_assert(kRowsHeld * E >= 4, "the groups' sums at the end fit the rows' places");
+  const int smem = groups * kRowsHeld * (int)LooseRow<E>::place(a.H);
+  const cudaError_t e = allow_shared<kRowsHeld * kLoosePlaces<NC, E, NT>>(kern, smem);
   if (e != cudaSuccess) return e;
   const Share sh = share_rows(a.T, R * groups, BLOCKS);
   *parts = sh.blocks;

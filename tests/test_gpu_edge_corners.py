@@ -2,6 +2,8 @@
 and that ordinary batches do not reach, against the fp64 oracle or the entry points themselves.
 """
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -76,6 +78,70 @@ def test_group_sums_beside_the_largest_values(moe, E, groups, k):
     for n in (1, 2, 3):
         r = moe.Routing(k, "sigmoid", groups, n, 2, renormalize=False)
         check(moe, r, logits, bias.reshape(E))
+
+
+# ---- host threads ---------------------------------------------------------------------------
+def run_at_once(*calls, times=300):
+    """Each call many times over in a host thread of its own, on a stream of its own."""
+    errors, start = [], threading.Barrier(len(calls))
+
+    def loop(call):
+        try:
+            stream = torch.cuda.Stream()
+            start.wait()
+            for _ in range(times):
+                call(stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001 (shown by the assertion)
+            errors.append(e)
+
+    threads = [threading.Thread(target=loop, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[:3]
+
+
+@pytest.mark.parametrize("dtype,T,lengths", [
+    ("bf16", 640, (2304, 2880)), ("bf16", 640, (2305, 2881)), ("fp32", 640, (3400, 4096)),
+    ("fp32", 640, (4200, 8184)), ("bf16", 640, (4200, 8191))])
+def test_norm_of_two_lengths_in_two_threads(moe, dtype, T, lengths):
+    """Rows of different lengths that share a kernel, from two host threads at once: the library's
+    calls alone, one after another, which let the other thread run."""
+    L, dt = moe._lib, TYPES[dtype]
+    fmt = L.ROWS_FP32 if dtype == "fp32" else L.ROWS_BF16
+
+    def call(H):
+        x, y, d = (rows(T, H, dt, s).cuda() for s in range(3))
+        w = rows(1, H, dt, 4, 0.3, 1.0)[0].cuda()
+        f = moe.norm_forward(x, w, y=y)
+        dx, dw, db = moe.norm_backward(d, f.x_out, f.mean, f.rstd, w, g=y)
+        out, xo, mean, rstd, gx, gw, gb = (torch.empty_like(t) for t in (
+            f.out, f.x_out, f.mean, f.rstd, dx, dw, db))
+        ws = torch.empty(moe.norm_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+        p = [t.data_ptr() for t in (x, y, w, xo, out, mean, rstd, d, gx, gw, gb, ws)]
+        x_, y_, w_, xo_, out_, mean_, rstd_, d_, gx_, gw_, gb_, ws_ = p
+        dims, n = L.Norm(T, H, L.NORMS["layer"], 1e-5, fmt, fmt), ws.numel()
+
+        def once(stream):
+            s = stream.cuda_stream
+            L.check(L.lib.mxfp4_moe_norm_forward(dims, x_, None, y_, w_, None, xo_, None, out_,
+                                                 mean_, rstd_, s), "forward")
+            L.check(L.lib.mxfp4_moe_norm_backward(dims, d_, xo_, None, mean_, rstd_, w_, y_, gx_,
+                                                  gw_, gb_, ws_, n, s), "backward")
+
+        def same():
+            for a, b in ((out, f.out), (gx, dx), (gw, dw), (gb, db)):
+                assert torch.equal(a, b)
+            return x, y, w, d, ws, xo, mean, rstd  # alive until here
+        return once, same
+
+    pairs = [call(H) for H in lengths]
+    torch.cuda.synchronize()
+    run_at_once(*(p[0] for p in pairs), times=4000)
+    for _, same in pairs:
+        same()
 
 
 # ---- the norm's gradients of rows far from zero ---------------------------------------------
