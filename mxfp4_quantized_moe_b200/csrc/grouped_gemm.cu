@@ -868,9 +868,21 @@ bool encode_2d(EncodeTiledFn enc, CUtensorMap* m, CUtensorMapDataType type, cons
   const cuuint64_t strides[1] = {(cuuint64_t)cols * elem};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t es[2] = {1, 1};
-  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // The first CUDA call of this host thread: the driver's function does not take up the device's
+    // context by itself; a call of the runtime does.
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, grouped_gemm_kernel<kEpiDx, false, false>) != cudaSuccess)
+      return false;
+    r = encode();
+  }
+  return r == CUDA_SUCCESS;
 }
 
 }  // namespace

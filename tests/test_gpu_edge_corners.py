@@ -81,6 +81,45 @@ def test_group_sums_beside_the_largest_values(moe, E, groups, k):
 
 
 # ---- host threads ---------------------------------------------------------------------------
+def test_first_call_of_a_host_thread(moe):
+    """The library's calls take up the device's context in a host thread that has made no CUDA
+    call yet, the ones that describe their operands to the driver first among them."""
+    from mxfp4_quantized_moe_b200 import inputs
+    L = moe._lib
+    T, H, I, E, k = 40, 64, 64, 4, 2
+    inp = inputs.make_layer(T, H, I, E, k, 9)
+    shape, w = moe.MoeShape(T, H, I, E, k), moe.weights_to(inp, "cuda")
+    ws, wt = moe.alloc_workspace(shape), moe.transpose_weights(shape, w)
+    x, dy = inp["x"].cuda(), inp["dy"].cuda()
+    lg = inp["logits"].cuda()
+    off = torch.tensor([0, 5, 20, 20, 40], dtype=torch.int32).cuda()
+    y = moe.forward(shape, w, x, lg, ws)
+    dx, dw, dl = moe.backward_input(shape, w, wt, dy, ws)
+    p = moe.grouped_matmul(off, x, w["gu_blocks"], w["gu_scales"], 2 * I)
+    moe.forward(shape, w, x, lg, ws)  # the state that the backward used up
+    outs = [torch.empty_like(t) for t in (y, dx, dw, dl, p)]
+    yp, dxp, dwp, dlp, pp = (t.data_ptr() for t in outs)
+    dims, weights = shape.dims(), moe._weights(w)
+    calls = {
+        "grouped_matmul": (E, 2 * I, H, T, off.data_ptr(), x.data_ptr(), w["gu_blocks"].data_ptr(),
+                           w["gu_scales"].data_ptr(), 0, pp, None, None),
+        "backward_input": (dims, weights, wt.data_ptr(), wt.numel(), dy.data_ptr(), ws.data_ptr(),
+                           ws.numel(), dxp, dwp, dlp, None),
+        "forward": (dims, weights, x.data_ptr(), lg.data_ptr(), yp, None, None, ws.data_ptr(),
+                    ws.numel(), None),
+    }
+    torch.cuda.synchronize()
+    for name, args in calls.items():
+        got = []
+        t = threading.Thread(target=lambda: got.append(getattr(L.lib, "mxfp4_moe_" + name)(*args)))
+        t.start()
+        t.join()
+        assert got == [L.OK], name
+    torch.cuda.synchronize()
+    for a, b in zip(outs, (y, dx, dw, dl, p)):
+        assert torch.equal(a, b)
+
+
 def run_at_once(*calls, times=300):
     """Each call many times over in a host thread of its own, on a stream of its own."""
     errors, start = [], threading.Barrier(len(calls))
