@@ -844,6 +844,8 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
+constexpr int kBlockSmem = 227 * 1024;  // shared memory that a block may ask for on sm_100
+
 template <int EPI, bool COLT, bool BS>
 cudaError_t launch_one(const CUtensorMap& tt, const CUtensorMap& tl, const CUtensorMap& tw,
                        const GemmArgs& a, int grid, size_t smem, cudaStream_t st) {
@@ -853,8 +855,11 @@ cudaError_t launch_one(const CUtensorMap& tt, const CUtensorMap& tl, const CUten
   cudaError_t fe = cudaFuncGetAttributes(&fa, kern);
   if (fe != cudaSuccess) return fe;
   if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  // The limit belongs to the kernel, and other host threads launch it with another K: every call
+  // sets the same one, all that a block can have.
+  const int most = kBlockSmem - (int)fa.sharedSizeBytes;
+  if (smem > (size_t)most) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, st>>>(tt, tl, tw, a);
   return cudaGetLastError();

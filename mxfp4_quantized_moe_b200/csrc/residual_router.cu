@@ -298,8 +298,10 @@ cudaError_t launch_grad_chain(int T, int H, int E, const uint16_t* g, const uint
                               cudaStream_t st) {
   if (T == 0) return cudaSuccess;
   const size_t smem = grad_chain_smem_bytes(E);
+  // the limit belongs to the kernel, and other host threads launch it with another E: every call
+  // sets the same one, that of the most experts
   cudaError_t e = cudaFuncSetAttribute(grad_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)grad_chain_smem_bytes(256));
   if (e != cudaSuccess) return e;
   grad_chain_kernel<<<(T + kGCTok - 1) / kGCTok, kThreads, smem, st>>>(T, H, E, g, dx, d_logits,
                                                                        w_r, g_out);

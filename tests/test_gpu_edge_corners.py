@@ -183,6 +183,41 @@ def test_norm_of_two_lengths_in_two_threads(moe, dtype, T, lengths):
         same()
 
 
+def test_products_and_gradient_chains_in_two_threads(moe):
+    """The experts' product with two K, and the gradient chain with two E, from two host threads:
+    the launches of one leave the other's limits alone."""
+    L, gen = moe._lib, torch.Generator().manual_seed(5)
+    off = torch.tensor([0, 20, 64], dtype=torch.int32).cuda()
+
+    def product(K, E):
+        x = torch.randn(64, K, generator=gen).bfloat16().cuda()
+        blocks = torch.randint(0, 256, (2, 64, K // 2), generator=gen, dtype=torch.uint8).cuda()
+        scales = torch.randint(120, 130, (2, 64, K // 32), generator=gen, dtype=torch.uint8).cuda()
+        g = torch.randn(64, 256, generator=gen).bfloat16().cuda()
+        dl = torch.randn(64, E, generator=gen).cuda()
+        w_r = torch.randn(256, E, generator=gen).bfloat16().cuda()
+        want = moe.grouped_matmul(off, x, blocks, scales, 64), moe.grad_chain(g, None, dl, w_r)
+        out = [torch.empty_like(t) for t in want]
+        held = (off, x, blocks, scales, g, dl, w_r, *out)
+        off_, x_, blocks_, scales_, g_, dl_, w_, out_, chain_ = (t.data_ptr() for t in held)
+
+        def once(stream):
+            s = stream.cuda_stream
+            L.check(L.lib.mxfp4_moe_grouped_matmul(2, 64, K, 64, off_, x_, blocks_, scales_, 0, out_,
+                                                   None, s), "product")
+            L.check(L.lib.mxfp4_moe_grad_chain(64, 256, E, g_, None, dl_, w_, chain_, s), "chain")
+
+        def same():
+            assert all(torch.equal(a, b) for a, b in zip(held[-2:], want))
+        return once, same
+
+    pairs = [product(128, 16), product(2880, 256)]
+    torch.cuda.synchronize()
+    run_at_once(*(p[0] for p in pairs), times=4000)
+    for _, same in pairs:
+        same()
+
+
 # ---- the norm's gradients of rows far from zero ---------------------------------------------
 @pytest.mark.parametrize("H", [64, 512, 4384])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
