@@ -16,9 +16,10 @@ Around the block, in the same graph:
     idx, w = route(logits, routing, bias)         # moe.Routing: scores, groups, balance bias
     y = moe_block_routed(n, idx, w, layer)        # the block on that routing
 
-norm(..., checkpoint="e4m3" | "int8") keeps the rows for the backward in 8 bits.  The backwards of
-these cannot be captured into a CUDA graph (an eager graph over the same leaves would end the
-process); capture moe.norm_backward, moe.route_backward and moe.backward_input instead.
+norm(..., checkpoint="e4m3" | "int8") keeps the rows for the backward in 8 bits, as the stack does.
+The backwards of these cannot be captured into a CUDA graph (an eager graph over the same leaves
+would end the process); capture moe.norm_backward, moe.route_backward and moe.backward_input
+instead.
 
 Source: "Add MXFP4 training support via a dequantize-on-the-fly fallback" (sections "What this
 does" and "Relation to the backward triton kernels": gradients reach the inputs through the
@@ -147,8 +148,10 @@ class _Norm(torch.autograd.Function):
         kept = rows if y is None else f.x_out
         if checkpoint:
             kept, ctx.scales, ctx.format = f.checkpoint.codes, f.checkpoint.scales, checkpoint
-        ctx.save_for_backward(kept, f.mean, f.rstd, w)
-        ctx.kind, ctx.checkpoint, ctx.shape = kind, checkpoint, x.shape
+            ctx.save_for_backward(kept, w)
+        else:
+            ctx.save_for_backward(kept, w, f.mean, f.rstd)
+        ctx.kind, ctx.eps, ctx.checkpoint, ctx.shape = kind, eps, checkpoint, x.shape
         ctx.bias_type = None if bias is None else bias.dtype
         out = f.out.view(x.shape)
         return out if residual is None else (out, f.x_out.view(x.shape))
@@ -157,8 +160,16 @@ class _Norm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_out, d_x_out=None):
         _refuse_capture("norm", "moe.norm_backward")
-        kept, mean, rstd, w = ctx.saved_tensors
-        rows = moe.Checkpoint(kept, ctx.scales, ctx.format) if ctx.checkpoint else kept
+        if ctx.checkpoint:
+            # the gradient at the rows that are kept: x_hat has mean 0 and variance 1 only with
+            # their own statistics
+            kept, w = ctx.saved_tensors
+            rows = moe.Checkpoint(kept, ctx.scales, ctx.format)
+            f = moe.norm_forward(rows, kind=ctx.kind, eps=ctx.eps, dtype=d_out.dtype)
+            mean, rstd = f.mean, f.rstd
+        else:
+            kept, w, mean, rstd = ctx.saved_tensors
+            rows = kept
         shape = kept.shape
         g = None if d_x_out is None else d_x_out.contiguous().view(shape)
         params = (w is not None and ctx.needs_input_grad[1]) or ctx.needs_input_grad[2]
@@ -178,6 +189,7 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor
          checkpoint: str | None = None):
     """Layer or rms norm over the last dimension of x (bf16 or fp32), with gradients to x, weight,
     bias and residual.  With a residual: (norm(x + residual), x + residual).  checkpoint ("e4m3" or
-    "int8", the last dimension a multiple of 32): the backward reads the rows from 8 bits, with
-    the statistics of the exact rows."""
+    "int8", the last dimension a multiple of 32): the rows are kept in 8 bits, and the backward is
+    the norm's gradient at the rows that these stand for (one more pass over them, for their
+    statistics)."""
     return _Norm.apply(x, weight, bias, residual, kind, eps, checkpoint)

@@ -8,7 +8,9 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_norm import R, TYPES, f64, rows
+from oracle import edge_oracle as O
+
+from test_gpu_norm import R, TYPES, check_backward, f64, hat_bound, rows
 from test_gpu_routing import check, normal
 
 pytestmark = pytest.mark.gpu
@@ -249,3 +251,38 @@ def test_gradient_of_constant_rows_of_large_values(moe, H, dtype, value, eps):
             assert np.all(np.abs(f64(dx) - ref) <= tol)
             assert not dw.any()
             assert np.all(np.abs(f64(db) - v.sum(0)) <= 4 * R * np.abs(v).sum(0))
+
+
+# ---- autograd forms -------------------------------------------------------------------------
+@pytest.mark.parametrize("format", ["e4m3", "int8"])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_autograd_norm_from_a_checkpoint_is_the_gradient_at_its_rows(moe, kind, format, dtype):
+    """The forward is that of the exact rows; the backward is the norm's gradient at the rows that
+    the checkpoint stands for, statistics included."""
+    from mxfp4_quantized_moe_b200.autograd import norm
+    T, H, dt = 70, 96, TYPES[dtype]
+    x, y, d, g = (rows(T, H, dt, s, 2.0, 0.5) for s in range(4))
+    w = rows(1, H, dt, 4, 0.3, 1.0)[0]
+    for residual in (False, True):
+        leaves = [t.cuda().requires_grad_(True) for t in ((x, w, y) if residual else (x, w))]
+        out = norm(leaves[0], leaves[1], residual=leaves[2] if residual else None, kind=kind,
+                   checkpoint=format)
+        n, xs = out if residual else (out, leaves[0])
+        ref = moe.norm_forward(xs.detach(), leaves[1].detach(), kind=kind)
+        assert torch.equal(n, ref.out)
+        torch.autograd.backward([n, xs] if residual else [n],
+                                [d.cuda(), g.cuda()] if residual else [d.cuda()])
+        _, _, v = O.checkpoint(f64(xs), format)
+        check_backward(leaves[0].grad, None, None, f64(d), v, f64(w), kind, dt,
+                       f64(g) if residual else None)
+        hat, mean, rstd = O.norm(v, kind=kind)
+        want = (f64(d) * hat).sum(0)
+        # 70 rows in sequence at most; then one rounding to the parameter's type
+        tol = (np.abs(f64(d)) * hat_bound(v, mean, rstd, kind)).sum(0)
+        tol = tol + 72 * R * np.abs(f64(d) * hat).sum(0)
+        tol = tol + torch.finfo(dt).eps / 2 * (np.abs(want) + tol)
+        assert np.all(np.abs(f64(leaves[1].grad) - want) <= tol)
+        if residual:
+            assert torch.equal(leaves[2].grad, leaves[0].grad)
+
