@@ -145,12 +145,10 @@ class _Norm(torch.autograd.Function):
         w = None if weight is None else weight.contiguous()
         f = moe.norm_forward(rows, w, None if bias is None else bias.contiguous(), kind=kind,
                              eps=eps, y=y, checkpoint=checkpoint)
-        kept = rows if y is None else f.x_out
         if checkpoint:
-            kept, ctx.scales, ctx.format = f.checkpoint.codes, f.checkpoint.scales, checkpoint
-            ctx.save_for_backward(kept, w)
+            ctx.save_for_backward(f.checkpoint.codes, f.checkpoint.scales, w)
         else:
-            ctx.save_for_backward(kept, w, f.mean, f.rstd)
+            ctx.save_for_backward(rows if y is None else f.x_out, w, f.mean, f.rstd)
         ctx.kind, ctx.eps, ctx.checkpoint, ctx.shape = kind, eps, checkpoint, x.shape
         ctx.bias_type = None if bias is None else bias.dtype
         out = f.out.view(x.shape)
@@ -163,8 +161,8 @@ class _Norm(torch.autograd.Function):
         if ctx.checkpoint:
             # the gradient at the rows that are kept: x_hat has mean 0 and variance 1 only with
             # their own statistics
-            kept, w = ctx.saved_tensors
-            rows = moe.Checkpoint(kept, ctx.scales, ctx.format)
+            kept, scales, w = ctx.saved_tensors
+            rows = moe.Checkpoint(kept, scales, ctx.checkpoint)
             f = moe.norm_forward(rows, kind=ctx.kind, eps=ctx.eps, dtype=d_out.dtype)
             mean, rstd = f.mean, f.rstd
         else:

@@ -286,3 +286,23 @@ def test_autograd_norm_from_a_checkpoint_is_the_gradient_at_its_rows(moe, kind, 
         if residual:
             assert torch.equal(leaves[2].grad, leaves[0].grad)
 
+
+
+def test_saved_tensor_hooks_see_all_that_is_kept(moe):
+    """Offloading what the graph keeps takes the checkpoint's scales along with its codes."""
+    from mxfp4_quantized_moe_b200.autograd import norm
+    x = rows(6, 64, torch.bfloat16, 1).cuda().requires_grad_(True)
+    seen = []
+
+    def pack(t):
+        seen.append((tuple(t.shape), t.dtype))
+        return t.cpu()
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t.cuda()):
+        out = norm(x, checkpoint="int8")
+    assert ((6, 64), torch.uint8) in seen and ((6, 2), torch.uint8) in seen
+    assert not any(isinstance(v, torch.Tensor) for v in vars(out.grad_fn).values())
+    out.backward(torch.ones_like(out))
+    first, x.grad = x.grad, None
+    norm(x, checkpoint="int8").backward(torch.ones_like(out))
+    assert torch.equal(first, x.grad)
