@@ -145,14 +145,17 @@ class _Norm(torch.autograd.Function):
         w = None if weight is None else weight.contiguous()
         f = moe.norm_forward(rows, w, None if bias is None else bias.contiguous(), kind=kind,
                              eps=eps, y=y, checkpoint=checkpoint)
+        # fresh tensors in x's shape, no views of them: a view that a Function returns may not be
+        # changed in place
+        out = f.out.resize_(x.shape)
+        x_out = None if y is None else f.x_out.resize_(x.shape)
         if checkpoint:
             ctx.save_for_backward(f.checkpoint.codes, f.checkpoint.scales, w)
         else:
-            ctx.save_for_backward(rows if y is None else f.x_out, w, f.mean, f.rstd)
+            ctx.save_for_backward(rows if y is None else x_out, w, f.mean, f.rstd)
         ctx.kind, ctx.eps, ctx.checkpoint, ctx.shape = kind, eps, checkpoint, x.shape
         ctx.bias_type = None if bias is None else bias.dtype
-        out = f.out.view(x.shape)
-        return out if residual is None else (out, f.x_out.view(x.shape))
+        return out if residual is None else (out, x_out)
 
     @staticmethod
     @once_differentiable
@@ -167,7 +170,7 @@ class _Norm(torch.autograd.Function):
             mean, rstd = f.mean, f.rstd
         else:
             kept, w, mean, rstd = ctx.saved_tensors
-            rows = kept
+            rows = kept = kept.view(-1, kept.shape[-1])
         shape = kept.shape
         g = None if d_x_out is None else d_x_out.contiguous().view(shape)
         params = (w is not None and ctx.needs_input_grad[1]) or ctx.needs_input_grad[2]

@@ -306,3 +306,33 @@ def test_saved_tensor_hooks_see_all_that_is_kept(moe):
     first, x.grad = x.grad, None
     norm(x, checkpoint="int8").backward(torch.ones_like(out))
     assert torch.equal(first, x.grad)
+
+
+@pytest.mark.parametrize("shape", [(6, 64), (2, 3, 64), (0, 64)])
+@pytest.mark.parametrize("checkpoint", [None, "e4m3"])
+def test_autograd_outputs_may_be_changed_in_place(moe, shape, checkpoint):
+    """As torch's own norms allow; a stream that the backward still reads is refused there."""
+    from mxfp4_quantized_moe_b200.autograd import norm
+    x = torch.randn(shape, device="cuda", requires_grad=True)
+    y = torch.randn(shape, device="cuda", requires_grad=True)
+    d = torch.randn(shape, device="cuda")
+
+    def grads(change):
+        x.grad = y.grad = None
+        n = norm(x, checkpoint=checkpoint)
+        n = n.mul_(2.0) if change else n * 2.0
+        m, s = norm(x, residual=y, checkpoint=checkpoint)
+        m = m.add_(1.0) if change else m + 1.0
+        assert n.shape == m.shape == s.shape == shape
+        (n + m * 3.0).backward(d)
+        return x.grad, y.grad
+
+    for a, b in zip(grads(True), grads(False)):
+        assert torch.equal(a, b)
+    m, s = norm(x, residual=y, checkpoint=checkpoint)
+    s.mul_(2.0)
+    if checkpoint:  # the rows are kept in 8 bits, the stream itself is free
+        (m + s).sum().backward()
+    else:
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            (m + s).sum().backward()
