@@ -269,6 +269,12 @@ def _tensor(t: torch.Tensor, name: str, shape, dtypes, index: int) -> int:
     return p or _EMPTY
 
 
+def _aligned(t: torch.Tensor | None):
+    """An input beside a checkpoint, which the kernels read in 16-byte vectors: t, or its copy where
+    t begins off such an address (a slice of a larger buffer)."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.detach().clone()
+
+
 @dataclass
 class Routing:
     """How tokens choose their experts (mxfp4_moe_routing in include/mxfp4_moe.h)."""
@@ -448,6 +454,7 @@ def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | Non
         with where:
             return checkpoint_pack(x, format, out)
     dev = t.get_device()
+    x = _aligned(x)
     xp = _tensor(x, "x", (T, H), _ROWS, dev)
     if out is None:
         out = Checkpoint._beside(x, format)
@@ -516,7 +523,9 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
 
     x: bf16 or fp32 rows, or a Checkpoint (normalised as the rows it stands for, into `dtype`,
     bf16 by default).  y: a residual; x_out = x + y, rounded to the rows' type, is returned and
-    is what is normalised.  checkpoint: a format or a Checkpoint to fill with those rows."""
+    is what is normalised.  checkpoint: a format or a Checkpoint to fill with those rows.  With a
+    checkpoint, outputs that the caller gives begin at 16-byte addresses, and inputs that do not
+    are copied first."""
     stored = isinstance(x, Checkpoint)
     if (stream is None and out is None and x_out is None and mean is None and rstd is None
             and not isinstance(checkpoint, Checkpoint)):
@@ -556,6 +565,9 @@ def norm_forward(x: torch.Tensor | Checkpoint, weight: torch.Tensor | None = Non
     dev = t.get_device()
     rows, own = (T, H), (dtype,)
     xp = frm = yp = op = mp = to = None
+    if stored or checkpoint is not None:
+        x = x if stored else _aligned(x)
+        y, weight, bias = _aligned(y), _aligned(weight), _aligned(bias)
     if stored:
         frm = x._abi(T, H, dev)
     else:
@@ -604,7 +616,8 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     x: the rows that were normalised (x_out where a residual was added), or their checkpoint with
     the statistics of the forward on it.  g: the residual stream's gradient, added to dx (dx may
     be g itself).  params=False computes dx alone and returns None for the other two; d_bias is
-    None for "rms" unless a tensor is given.  ws: scratch of norm_workspace_bytes (else
+    None for "rms" unless a tensor is given.  With a checkpoint, dx begins at a 16-byte address, and
+    inputs that do not are copied first.  ws: scratch of norm_workspace_bytes (else
     allocated); two captured graphs that may run at once need one each."""
     if (stream is None and params and dx is None and d_weight is None and d_bias is None
             and ws is None):
@@ -628,6 +641,8 @@ def norm_backward(d_out: torch.Tensor, x: torch.Tensor | Checkpoint, mean: torch
     dev = t.get_device()
     rows, own = (T, H), (dtype,)
     xp = frm = dwp = dbp = wsp = None
+    if isinstance(x, Checkpoint):
+        d_out, weight, g = _aligned(d_out), _aligned(weight), g if g is dx else _aligned(g)
     dp = _tensor(d_out, "d_out", rows, _ROWS, dev)
     if isinstance(x, Checkpoint):
         frm = x._abi(T, H, dev)

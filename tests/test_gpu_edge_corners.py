@@ -336,3 +336,44 @@ def test_autograd_outputs_may_be_changed_in_place(moe, shape, checkpoint):
     else:
         with pytest.raises(RuntimeError, match="modified by an inplace"):
             (m + s).sum().backward()
+
+
+# ---- checkpoints beside tensors without 16-byte alignment -----------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_inputs_at_any_address_with_a_checkpoint(moe, dtype):
+    """Rows and parameters that are slices of larger buffers, wherever they begin."""
+    from mxfp4_quantized_moe_b200.autograd import norm
+    T, H, dt = 5, 96, TYPES[dtype]
+
+    def at(t, off):  # a copy that begins off elements behind an aligned address
+        buf = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")
+        buf[off:].copy_(t.reshape(-1))
+        return buf[off:].view(t.shape)
+
+    base = [rows(T, H, dt, s).cuda() for s in range(4)]
+    params = [rows(1, H, dt, s, 0.3, 1.0)[0].cuda() for s in (4, 5)]
+    x, y, d, g = base
+    f = moe.norm_forward(x, *params, y=y, checkpoint="int8")
+    n = moe.norm_forward(f.checkpoint, *params, dtype=dt)
+    b = moe.norm_backward(d, f.checkpoint, n.mean, n.rstd, params[0], g=g)
+    for off in (1, 3):
+        (xo, yo, do, go), po = [at(t, off) for t in base], [at(t, off) for t in params]
+        assert xo.data_ptr() % 16
+        f2 = moe.norm_forward(xo, *po, y=yo, checkpoint="int8")
+        n2 = moe.norm_forward(f2.checkpoint, *po, dtype=dt)
+        b2 = moe.norm_backward(do, f2.checkpoint, n2.mean, n2.rstd, po[0], g=go)
+        for p, q in ((f.out, f2.out), (f.x_out, f2.x_out), (f.checkpoint.codes, f2.checkpoint.codes),
+                     (f.checkpoint.scales, f2.checkpoint.scales), (n.out, n2.out), *zip(b, b2)):
+            assert torch.equal(p, q)
+        assert torch.equal(moe.checkpoint_pack(xo, "e4m3").codes, moe.checkpoint_pack(x, "e4m3").codes)
+        xl, wl = xo.detach().requires_grad_(True), po[0].detach().requires_grad_(True)
+        out = norm(xl, wl, po[1], residual=yo, checkpoint="int8")
+        torch.autograd.backward(out, [do, go])
+        assert torch.equal(out[0], f.out) and torch.equal(xl.grad, b[0])
+        # the gradient added in place stays in place
+        g3 = at(g, off)
+        with pytest.raises(moe._lib.MoeError):
+            moe.norm_backward(do, f.checkpoint, n.mean, n.rstd, params[0], g=g3, dx=g3)
+        # outputs of the caller are not copied: refused as before
+        with pytest.raises(moe._lib.MoeError):
+            moe.norm_forward(x, out=xo, checkpoint="int8")
