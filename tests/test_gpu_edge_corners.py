@@ -10,7 +10,7 @@ import torch
 
 from oracle import edge_oracle as O
 
-from test_gpu_norm import R, TYPES, check_backward, f64, hat_bound, rows
+from test_gpu_norm import R, TYPES, check_backward, check_forward, f64, hat_bound, rows
 from test_gpu_routing import check, normal
 
 pytestmark = pytest.mark.gpu
@@ -377,3 +377,55 @@ def test_inputs_at_any_address_with_a_checkpoint(moe, dtype):
         # outputs of the caller are not copied: refused as before
         with pytest.raises(moe._lib.MoeError):
             moe.norm_forward(x, out=xo, checkpoint="int8")
+
+
+# ---- many rows with checkpoints -------------------------------------------------------------
+def stored(x, format):
+    """Codes, scale bytes and values of finite rows by the definition, block by block of 32."""
+    b = x.double().view(x.shape[0], -1, 32)
+    limit, bias = (448.0, 127) if format == "e4m3" else (127.0, 133)
+    most = b.abs().amax(2, keepdim=True)
+    m, e = torch.frexp(most / limit)
+    S = torch.where(m > 0.5, e, e - 1)  # the least S with most <= limit 2^S
+    S = torch.where(most > 0, S, -126).clamp(min=-126)
+    v = torch.ldexp(b, -S)
+    if format == "e4m3":
+        v = v.float().to(torch.float8_e4m3fn)
+        codes, v = v.view(torch.uint8), v.double()
+    else:
+        v = v.round()
+        codes = v.to(torch.int8).view(torch.uint8)
+    return (codes.view(x.shape), (S + bias).to(torch.uint8).view(x.shape[0], -1),
+            torch.ldexp(v, S).view(x.shape))
+
+
+@pytest.mark.parametrize("format", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,kind", [("bf16", "layer"), ("fp32", "rms")])
+@pytest.mark.parametrize("T,H", [(601, 32), (15003, 96), (15003, 256), (4001, 1056), (1501, 2880),
+                                 (1301, 4096), (623, 6144), (611, 8192), (603, 16384)])
+def test_many_rows_beside_and_from_a_checkpoint(moe, T, H, kind, dtype, format):
+    """Batches of several turns of the persistent forms, the last one ragged: the checkpoint that
+    the forward fills, the norm from it, and the gradients from it."""
+    dt = TYPES[dtype]
+    x, y, d, g = (rows(T, H, dt, s, 2.0).cuda() for s in range(4))
+    # magnitudes differ from block to block, so that no block's scale serves its neighbour
+    x *= torch.exp2((torch.arange(H, device="cuda") // 32 % 5).to(dt))
+    x *= torch.exp2((torch.arange(T, device="cuda") % 7).to(dt))[:, None]
+    w = rows(1, H, dt, 4, 0.3, 1.0)[0].cuda()
+    xs = (x.float() + y.float()).to(dt)
+    f = moe.norm_forward(x, w, kind=kind, y=y, checkpoint=format)
+    codes, scales, values = stored(xs.cpu(), format)
+    assert torch.equal(f.x_out, xs)
+    assert torch.equal(f.checkpoint.codes.cpu(), codes)
+    assert torch.equal(f.checkpoint.scales.cpu(), scales)
+    check_forward(f.out, f.mean, f.rstd, f64(xs), f64(w), None, kind, dt)
+    kept = moe.norm_forward(xs, w, kind=kind, checkpoint=format)  # no residual
+    assert torch.equal(kept.checkpoint.codes.cpu(), codes) and torch.equal(kept.out, f.out)
+    assert torch.equal(kept.checkpoint.scales.cpu(), scales)
+    v = values.numpy()
+    n = moe.norm_forward(f.checkpoint, w, kind=kind, dtype=dt)
+    check_forward(n.out, n.mean, n.rstd, v, f64(w), None, kind, dt)
+    dx, dw, db = moe.norm_backward(d, f.checkpoint, n.mean, n.rstd, w, kind=kind, g=g)
+    check_backward(dx, dw, db, f64(d), v, f64(w), kind, dt, f64(g))
+    dx, _, _ = moe.norm_backward(d, f.checkpoint, n.mean, n.rstd, w, kind=kind)
+    check_backward(dx, None, None, f64(d), v, f64(w), kind, dt)
