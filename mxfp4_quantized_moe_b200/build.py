@@ -5,8 +5,10 @@
   indices they read from the workspace and record MXFP4_MOE_ERR_DEVICE_BOUNDS instead of
   making the access (``mxfp4_moe_build_flags`` reports the build).  Loaded instead of the
   library when ``MXFP4_MOE_LIBRARY=debug``.
-* ``_edge.so``: the host side of the operators at the block's edge as a CPython module
-  (csrc/binding.cpp), which calls whichever of the two is loaded.
+* ``_edge.<torch>.<python>.so``: the host side of the operators at the block's edge as a CPython
+  module (csrc/binding.cpp), which calls whichever of the two is loaded.  It is compiled against
+  the headers of one torch and one Python, and its name says which: under others it is built anew,
+  not loaded.
 
 Usage: ``python -m mxfp4_quantized_moe_b200.build [--verbose-ptxas]`` builds all three.  Cross-compiles
 without a GPU.  The libraries statically link the CUDA runtime, so they load on a machine
@@ -15,6 +17,7 @@ without a driver (calls then fail with MXFP4_MOE_ERR_CUDA).
 
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -28,7 +31,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmxfp4_moe.so")
 LIB_DEBUG = os.path.join(HERE, "libmxfp4_moe_debug.so")
 BINDING_SOURCE = os.path.join("csrc", "binding.cpp")
-BINDING = os.path.join(HERE, "_edge.so")
+BINDING = os.path.join(HERE, f"_edge.torch-{importlib.metadata.version('torch')}."
+                             f"{sysconfig.get_config_var('SOABI')}.so")
 SOURCES = ["csrc/api.cu", "csrc/grouped_gemm.cu", "csrc/kernels_small.cu",
            "csrc/forward_static.cu", "csrc/selftest.cu", "csrc/residual_router.cu",
            "csrc/routing.cu", "csrc/norm.cu"]

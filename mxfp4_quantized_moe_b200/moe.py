@@ -8,15 +8,32 @@ library's kernels.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from dataclasses import dataclass
 from functools import lru_cache
 from typing import NamedTuple
 
 import torch
 
-from . import _edge, _lib
+from . import _lib, build
 from ._lib import Dims, Weights, check, lib
 
+
+def _load_edge():
+    """The binding module of this torch and Python (csrc/binding.cpp); like the library, it fails
+    loudly where it is missing."""
+    if not os.path.exists(build.BINDING):
+        raise ImportError(
+            f"{build.BINDING} is missing: build it with `python -m mxfp4_quantized_moe_b200.build` "
+            "(there is no fallback implementation)")
+    spec = importlib.util.spec_from_file_location(f"{__package__}._edge", build.BINDING)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_edge = _load_edge()
 _edge.bind(*(ctypes.cast(getattr(lib, "mxfp4_moe_" + name), ctypes.c_void_p).value for name in (
     "route", "route_backward", "norm_forward", "norm_workspace_size", "norm_backward",
     "checkpoint_pack", "checkpoint_unpack")))
