@@ -286,6 +286,13 @@ def _tensor(t: torch.Tensor, name: str, shape, dtypes, index: int) -> int:
     return p or _EMPTY
 
 
+def _int32(**sizes: int) -> None:
+    """The library counts in 32 bits, and ctypes drops what does not fit."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def _aligned(t: torch.Tensor | None):
     """An input beside a checkpoint, which the kernels read in 16-byte vectors: t, or its copy where
     t begins off such an address (a slice of a larger buffer)."""
@@ -312,6 +319,7 @@ class Routing:
 def _routing_dims(T, E, k, scores, groups, top_groups, group_best, renormalize, scale):
     if scores not in _lib.SCORES:
         raise ValueError(f"scores must be one of {sorted(_lib.SCORES)}")
+    _int32(T=T, E=E, k=k, groups=groups, top_groups=top_groups, group_best=group_best)
     return _lib.Routing(T, E, k, _lib.SCORES[scores], groups, top_groups, group_best,
                         int(renormalize), scale)
 
@@ -319,6 +327,7 @@ def _routing_dims(T, E, k, scores, groups, top_groups, group_best, renormalize, 
 def _logits_shape(logits: torch.Tensor):
     if logits.dim() != 2:
         raise ValueError("logits must be fp32 [T, E]")
+    _int32(T=logits.shape[0], E=logits.shape[1])
     return logits.shape
 
 
@@ -449,6 +458,7 @@ def _rows_shape(x):
     t = x.codes if isinstance(x, Checkpoint) else x
     if t.dim() != 2:
         raise ValueError("rows must be [T, H]")
+    _int32(T=t.shape[0], H=t.shape[1])
     return (*t.shape, t)
 
 
@@ -524,6 +534,7 @@ def _norm_dims(T, H, kind, eps, rows: torch.dtype, params: torch.dtype) -> _lib.
 @lru_cache(maxsize=1024)
 def norm_workspace_bytes(T: int, H: int) -> int:
     """Scratch bytes of norm_backward with the parameters' gradients."""
+    _int32(T=T, H=H)
     n = ctypes.c_size_t()
     check(lib.mxfp4_moe_norm_workspace_size(_lib.Norm(T, H, 0, 0.0, 0, 0), n),
           "mxfp4_moe_norm_workspace_size")
