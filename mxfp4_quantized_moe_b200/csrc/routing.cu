@@ -218,6 +218,8 @@ MOE_DEV bool select(const RouteArgs& a, const Token<NG>& t, F* buf, Picked<NS>& 
     const bool mine = lane < a.groups;
     const unsigned kept = __ballot_sync(kFull, mine && rank < a.top_groups);
     if (fast && (approx || a.best2) && a.top_groups < a.groups) {
+      // a sum below what fp32 holds is not that of a group without experts
+      if (__any_sync(kFull, mine && m1 > (F)-INFINITY && !(score > (F)-INFINITY))) return false;
       // every kept group must lie above every other one (those without experts, at -inf, do not
       // count) by what both may be off
       const bool some = mine && score > (F)-INFINITY;
@@ -561,6 +563,8 @@ __global__ void __launch_bounds__(128, NS == 32 ? 6 : 8) route4_kernel(RouteArgs
     }
     const bool real = q < a.groups, kept = real && rank < a.top_groups;
     if (scored) {
+      // (a sum below the lowest finite value ranks behind groups without experts here; keys that
+      // low are beyond the words' range, and select() decides)
       const float in = min8(kept ? mine - slack : INFINITY);
       const float no = max8(real && !kept && mine > -FLT_MAX ? mine + slack : -INFINITY);
       unsure |= no > -INFINITY && !(in > no);

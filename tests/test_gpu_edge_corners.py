@@ -82,6 +82,25 @@ def test_group_sums_beside_the_largest_values(moe, E, groups, k):
         check(moe, r, logits, bias.reshape(E))
 
 
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,k", [(8, 4, 2), (32, 4, 2), (64, 4, 4), (128, 8, 4), (40, 5, 1)])
+def test_group_sums_below_the_lowest_value(moe, E, groups, k, scores):
+    """Two keys may sum to less than fp32 holds: such a group still comes before one that has no
+    expert left, and after all others."""
+    logits = normal(40, E, E + 2)
+    size = E // groups
+    logits.view(-1, groups, size)[:, 0] = float("-inf")
+    logits.view(-1, groups, size)[::4, 3, 1:] = float("-inf")
+    low = torch.finfo(torch.float32).min
+    for level in (0.75 * low, 0.5 * low):
+        bias = normal(1, E, 43, 0.05)[0].view(groups, size)
+        bias[1:3] = level
+        for top_groups in range(1, groups + 1):
+            if top_groups * size >= k:
+                r = moe.Routing(k, scores, groups, top_groups, 2, renormalize=False)
+                check(moe, r, logits, bias.reshape(E))
+
+
 # ---- host threads ---------------------------------------------------------------------------
 def test_first_call_of_a_host_thread(moe):
     """The library's calls take up the device's context in a host thread that has made no CUDA
