@@ -218,16 +218,14 @@ MOE_DEV bool select(const RouteArgs& a, const Token<NG>& t, F* buf, Picked<NS>& 
     const bool mine = lane < a.groups;
     const unsigned kept = __ballot_sync(kFull, mine && rank < a.top_groups);
     if (fast && (approx || a.best2) && a.top_groups < a.groups) {
-      // a sum below what fp32 holds is not that of a group without experts
-      if (__any_sync(kFull, mine && m1 > (F)-INFINITY && !(score > (F)-INFINITY))) return false;
-      // every kept group must lie above every other one (those without experts, at -inf, do not
-      // count) by what both may be off
-      const bool some = mine && score > (F)-INFINITY;
+      // Every kept group must lie above every other one by what both may be off.  Groups without
+      // experts, at -inf, do not count; a sum below what fp32 holds is not one of those.
+      const bool some = mine && m1 > (F)-INFINITY, sunk = some && !(score > (F)-INFINITY);
       const float slack = some ? group_slack((float)m1, (float)m2, 0x1p-18f) : 0.f;
       const float low = mine && rank < a.top_groups ? (float)score - slack : INFINITY;
-      const float high = some && rank >= a.top_groups ? (float)score + slack : -INFINITY;
-      const float out = warp_maxf(high);
-      if (out > -INFINITY && !(-warp_maxf(-low) > out)) return false;
+      const float high = sunk ? INFINITY : some && rank >= a.top_groups ? (float)score + slack : -INFINITY;
+      const uint32_t out = warp_max(order_bits(high)), in = ~warp_max(~order_bits(low));
+      if (out > order_bits(-INFINITY) && in <= out) return false;
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {

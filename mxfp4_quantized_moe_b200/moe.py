@@ -327,8 +327,10 @@ def _routing_dims(T, E, k, scores, groups, top_groups, group_best, renormalize, 
 def _logits_shape(logits: torch.Tensor):
     if logits.dim() != 2:
         raise ValueError("logits must be fp32 [T, E]")
-    _int32(T=logits.shape[0], E=logits.shape[1])
-    return logits.shape
+    T, E = logits.shape
+    if T >= 2 ** 31 or E >= 2 ** 31:
+        _int32(T=T, E=E)
+    return T, E
 
 
 def route(routing: Routing, logits: torch.Tensor, bias: torch.Tensor | None = None,
@@ -458,8 +460,10 @@ def _rows_shape(x):
     t = x.codes if isinstance(x, Checkpoint) else x
     if t.dim() != 2:
         raise ValueError("rows must be [T, H]")
-    _int32(T=t.shape[0], H=t.shape[1])
-    return (*t.shape, t)
+    T, H = t.shape
+    if T >= 2 ** 31 or H >= 2 ** 31:
+        _int32(T=T, H=H)
+    return T, H, t
 
 
 def _format(dtype: torch.dtype) -> int:
