@@ -43,6 +43,8 @@
  *    are detected before anything is enqueued.  Faults detected on the device (a bounded wait
  *    that expired, an index out of range) are written to an error word inside the workspace
  *    and reported by mxfp4_moe_check.
+ *  - Several host threads may call at once, each with outputs and workspaces of its own, except
+ *    mxfp4_moe_forward_static and the profiling calls (see there).
  *  - The current CUDA device must be an sm_100 part (B200); otherwise
  *    MXFP4_MOE_ERR_UNSUPPORTED_DEVICE.
  *  - Shapes: H and I multiples of 32 (one MX block), 1 <= k <= E <= 256, T >= 1, A = T*k < 2^31.

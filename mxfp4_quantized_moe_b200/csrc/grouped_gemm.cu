@@ -41,6 +41,7 @@
 // dequantize-on-the-fly fallback" (section "What this does": the expert math over weights
 // dequantized on the fly; section "Relation to the backward triton kernels": input
 // gradients through the frozen weights, no weight gradient).
+#include <atomic>
 #include <cuda.h>
 
 #include "common.cuh"
@@ -832,14 +833,15 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
+  static std::atomic<EncodeTiledFn> known{nullptr};  // of several host threads
+  EncodeTiledFn fn = known.load();
   if (!fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
             cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+      known.store(fn = reinterpret_cast<EncodeTiledFn>(ptr));
   }
   return fn;
 }
