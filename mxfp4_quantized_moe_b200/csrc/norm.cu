@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) norm_forward_many_kernel(NormArgs 
 // (the last one with only its bytes of the row), what lies before the first of them by plain loads
 // of single features.  The row then stands at 16 - head bytes in its place, and a lane reads the
 // features lane, lane + 32, ... of every 256.  T = 16384, H = 1001, bf16: forward 24 us (2.7 TB/s),
-// backward 44 us; read feature by feature from global memory they took 64 and 62 us.
+// backward 40 us; read feature by feature from global memory they took 64 and 62 us.
 template <int E>  // bytes of a feature
 struct LooseRow {
   const uint8_t* from;
@@ -1478,9 +1478,17 @@ __global__ void __launch_bounds__(256) checkpoint_unpack_kernel(mxfp4_moe_checkp
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Rows of a batch from which the forward takes its persistent form: about two per warp group that
-// fits the GPU.  64 rows of 2880 take 2.7 us in the form for few rows, 32768 take 93 us in it and
-// 60 us in the persistent one.
+// Rows of a batch from which the forward takes its persistent form.  Few rows / persistent, bf16:
+//   rows        150        300        600       1200       2400   (32768 of 2880: 93 / 60 us)
+//   H = 256   2.0 / 2.6  2.1 / 2.7  2.2 / 2.7  2.2 / 2.8  3.0 / 2.8 us
+//   1024      2.5 / 3.0  2.6 / 3.1  3.7 / 3.1  5.2 / 3.2  8.1 / 3.8
+//   2880      2.7 / 3.1  3.3 / 3.1  4.9 / 3.6  7.6 / 4.8   13 / 6.5
+//   4096      3.1 / 2.8  4.5 / 3.3  6.6 / 4.2   11 / 5.6   19 / 8.7
+//   16384     6.3 / 5.3  8.8 / 7.0   14 / 10    24 / 16    56 / 32
+// The forms meet at about 2000 warps of the first one (T H / 256 up to H = 4096), so one number of
+// rows is a compromise: short rows lose 0.6 us from it on, rows of 4096 and more 1 to 4 us below
+// it.  fp32 rows with a residual meet later (600 rows of 2880: 7.0 / 9.5 us), rows without vector
+// alignment at 500 to 1000 (1001: 5.3 / 5.7).  Rows in L2, as a batch of this size just written is.
 constexpr int kManyRows = 600;
 
 // Leave for a launch of `bytes` of dynamic shared memory.  The leave belongs to the kernel, not to

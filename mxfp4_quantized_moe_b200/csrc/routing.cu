@@ -297,9 +297,12 @@ MOE_DEV bool select(const RouteArgs& a, const Token<NG>& t, F* buf, Picked<NS>& 
   return true;
 }
 
-// One warp per token, for k > 8 and groups that are no whole slots.  Reads 4 E bytes and writes 8 k
-// bytes a token; the k rounds of warp reductions bound it, not the bytes (T = 32768, E = 256, k = 8:
-// 61 us without a bias, 88 with one, against 14 and 21 in the form for four tokens below).
+// One warp per token, for k > 8 and for groups that are no whole slots or more than 8.  Reads 4 E
+// bytes and writes 8 k bytes a token; the k rounds of warp reductions bound it, and the scan of a
+// group by one lane, not the bytes.  T = 32768: E = 256, k = 8, without groups (forced into this
+// form) 61 us without a bias and 88 with one, against 14 and 21 in the form for four tokens below;
+// E = 160, k = 6, 3 of 8 groups 84 and 105 us; E = 256, k = 8, 4 of 32 groups with a bias 120 us;
+// k = 16 without groups 93 and 130 us.
 template <int NG, int NS>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a) {
   __shared__ double s_buf[kWarps][32 * NG];

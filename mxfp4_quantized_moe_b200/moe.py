@@ -474,7 +474,8 @@ def _format(dtype: torch.dtype) -> int:
 
 def checkpoint_pack(x: torch.Tensor, format: str = "e4m3", out: Checkpoint | None = None,
                     stream=None) -> Checkpoint:
-    """Rows [T, H] (bf16 or fp32, H a multiple of 32) stored in 8 bits."""
+    """Rows [T, H] (bf16 or fp32, H a multiple of 32) stored in 8 bits, in `format`, or in `out` and
+    its format."""
     if stream is None and out is None:
         done = _edge.checkpoint_pack(x, format)
         if done is not None:
