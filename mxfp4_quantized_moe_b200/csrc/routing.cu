@@ -370,7 +370,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteArgs a) {
 // of the chosen experts and at most one other are compared in fp64; a token that needs more, or
 // has fewer than k unmasked experts, goes through select() instead.  Bound by the ALU pipe
 // (min / max, compares, selects: half its slots) and latency, not by the bytes.  T = 32768, E = 256,
-// k = 8: softmax 14 us, sigmoid with a bias 21 us, with 4 of 8 groups 27 us, where the logits'
+// k = 8: softmax 14 us, sigmoid with a bias 21 us, with 4 of 8 groups 26-28 us (by the draw: a
+// few rows go to fp64, and a wider margin, with more of them, measures slower), where the logits'
 // bytes alone take 5.4 us.
 template <int N>
 MOE_DEV void exchange(uint32_t (&v)[N], int i, int j) {  // the larger to i
